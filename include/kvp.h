@@ -73,7 +73,8 @@ extern "C" {
 #define KVP_BF16 1
 /* E4M3 codes (1 sign, 4 exponent, 3 mantissa bits, bias 7, largest 448, no
  * infinities) with per-KV-head fp32 scales: a pool of this type is written by
- * reshape_and_cache_fp8 and read by paged_attention_decode_fp8. */
+ * reshape_and_cache_fp8 or rope_reshape_and_cache and read by
+ * paged_attention_decode_fp8 or paged_attention_decode_sparse. */
 #define KVP_FP8_E4M3 2
 
 typedef struct kvp_pool kvp_pool;
@@ -585,6 +586,133 @@ KVP_API int paged_attention_decode_fp8(const void* q, const void* k_cache, const
                                        float scale, int32_t partition_size, void* workspace,
                                        size_t workspace_bytes, void* out, int32_t dtype,
                                        kvp_stream_t stream);
+
+/* ---- block-sparse decoding ---------------------------------------------
+ * One decode step over a long context, in four calls: the new tokens' queries
+ * and keys are rotated to their positions and the keys and values stored
+ * (rope_reshape_and_cache); the bounds of the blocks that changed are brought
+ * up to date (update_key_bounds); every (sequence, KV head) picks the blocks
+ * its queries need most by an upper bound on their logits (select_blocks); the
+ * attention reads those blocks only (paged_attention_decode_sparse), so its
+ * bytes do not grow with the context. Keys and values in blocks behind a table
+ * are what makes reading a subset of them cheap ["PagedAttention: KV cache
+ * memory management", section "How logical blocks, physical blocks and the
+ * block table work"].
+ * The pools are those of the 16-bit and the E4M3 cache. The bounds are a third
+ * pool with the blocks' numbering, key_bounds [num_blocks][num_kv_heads][2]
+ * [head_dim]: of each channel the largest valid key, then the smallest; of the
+ * cache's type, or fp16 values of the codes (before the scale) for an E4M3
+ * cache. The three calls that read bounds or lists take block_size 8, 16 or
+ * 32 and head_dim 64 or 128 (E4M3: 128). None of the four needs a workspace. */
+
+/* Rotates the queries and keys of num_tokens tokens and stores keys and values:
+ * with c_i = cos_sin[p][i], s_i = cos_sin[p][rot_dim/2 + i] of the token's
+ * position p = positions[t], channel pair (a, b) of every head becomes
+ *   a' = a c_i - b s_i,   b' = b c_i + a s_i,   i < rot_dim / 2,
+ * with (a, b) = (x[i], x[rot_dim/2 + i]) or, interleaved != 0, (x[2i],
+ * x[2i + 1]); channels from rot_dim on pass through, values are not rotated.
+ * The products and the sum are fp32, rounded to nearest one by one, and the
+ * result is rounded once to the stored type. Queries go to q_out, keys and
+ * values to slot slot_mapping[t] of the pools: 16-bit ones of dtype
+ * (cache_dtype == dtype), or E4M3 codes of the value over k_scale[h] /
+ * v_scale[h] as in reshape_and_cache_fp8 (cache_dtype KVP_FP8_E4M3).
+ * q: device [num_tokens][num_q_heads][head_dim], k_new, v_new: device
+ * [num_tokens][num_kv_heads][head_dim], q_out like q; q_stride and the others
+ * are the elements between two tokens (multiples of 8), so all three may lie
+ * in one projection's output. q_out may be q itself (with its stride) and may
+ * overlap neither k_new, v_new nor another part of q. cos_sin: device fp32
+ * [max_positions][rot_dim]; positions, slot_mapping: device int64. Pointers to
+ * rows, pools and table are 16-byte aligned.
+ * A token of a negative slot is padding: nothing is stored, and its query is
+ * rotated unless its position is negative too, in which case its row of q_out
+ * stays as it was. Skipped whole and recorded (KVP_ERR_BOUNDS): a position
+ * outside [0, max_positions) in any other token. Skipped keys and values and
+ * recorded: a slot past the pool. Two tokens of one slot leave either's data.
+ * head_dim / 16 (at most 64) and block_size are powers of two, rot_dim a
+ * multiple of 16 in [16, head_dim].
+ * Errors: KVP_ERR_INVALID (sizes, types, overlap, NULL or misaligned pointers). */
+KVP_API int rope_reshape_and_cache(const void* q, const void* k_new, const void* v_new, void* q_out,
+                                   int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                   int64_t q_out_stride, const float* cos_sin,
+                                   const int64_t* positions, int64_t max_positions,
+                                   int32_t rot_dim, int32_t interleaved, void* k_cache,
+                                   void* v_cache, const int64_t* slot_mapping,
+                                   const float* k_scale, const float* v_scale, int32_t num_tokens,
+                                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                   int32_t block_size, int32_t num_blocks, int32_t dtype,
+                                   int32_t cache_dtype, kvp_stream_t stream);
+
+/* Recomputes the bounds of each block that holds one of the newest
+ * new_tokens[s] tokens of sequence s (device int32 [num_seqs], entries in
+ * [0, max_new_tokens]; more than context_lens[s] means all of them), or of
+ * every block of the sequences (new_tokens NULL; max_new_tokens is not read):
+ *   key_bounds[b][h][0][d] = max_t k_cache[b][h][t][d], [1]: min_t,
+ * over the block's tokens below context_lens[s], whole, whatever the bounds
+ * held; so a block that copy-on-write gave a sequence needs no copy of its
+ * bounds, because the token that caused the copy is in it. Other blocks'
+ * bounds stay as they are. A NaN key makes its channel's bounds NaN. A block
+ * that several sequences list should hold as many valid tokens for each of
+ * them (as shared blocks do); else the bounds are those of one of them.
+ * Recorded: a length outside [0, max_context_len] (clamped), a count outside
+ * [0, max_new_tokens] (clamped), a block id outside the pool (skipped).
+ * Errors: KVP_ERR_INVALID (sizes, types, NULL or misaligned pointers). */
+KVP_API int update_key_bounds(const void* k_cache, void* key_bounds, const int32_t* block_tables,
+                              const int32_t* context_lens, const int32_t* new_tokens,
+                              int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t block_size, int32_t num_blocks, int32_t max_blocks_per_seq,
+                              int32_t max_context_len, int32_t max_new_tokens, int32_t cache_dtype,
+                              kvp_stream_t stream);
+
+/* For each sequence s and KV head h, the logical numbers of the blocks that
+ * its queries need most, selected [num_seqs][num_kv_heads][num_selected],
+ * ascending, -1 behind them: every block of a context of at most num_selected
+ * blocks; else the first num_sink, the last num_recent (their sum at most
+ * num_selected) and of the others the best by
+ *   score(b) = sum_d Q+[d] max_b[d] + Q-[d] min_b[d],
+ *   Q+ = sum_g max(q[g], 0),  Q- = sum_g min(q[g], 0)
+ * over the head's G = num_q_heads / num_kv_heads queries g, which is sum_g
+ * sum_d of the larger of q max_b and q min_b and so at least the sum over g of
+ * any logit q[g] . key of the block. Scores are summed in fp64; of equal scores
+ * the lowest block wins, and a NaN score (a NaN, or an infinite key where Q+ or
+ * Q- is zero) counts as the best, so that such a block is kept.
+ * With an E4M3 cache the key scale (positive) does not change the order and is
+ * left out. q: device [num_seqs][num_q_heads][head_dim] of dtype; key_bounds
+ * as above of cache_dtype (dtype or KVP_FP8_E4M3). A sequence with several new
+ * tokens takes a row for each, with the token's own length. A context has at
+ * most 212,992 blocks (max_context_len / block_size).
+ * Recorded: a length outside [0, max_context_len] (clamped), a block id
+ * outside the pool (scored last).
+ * Errors: KVP_ERR_INVALID (sizes, types, NULL or misaligned pointers). */
+KVP_API int select_blocks(const void* q, const void* key_bounds, const int32_t* block_tables,
+                          const int32_t* context_lens, int32_t* selected, int32_t num_seqs,
+                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                          int32_t block_size, int32_t num_blocks, int32_t max_blocks_per_seq,
+                          int32_t max_context_len, int32_t num_selected, int32_t num_sink,
+                          int32_t num_recent, int32_t dtype, int32_t cache_dtype,
+                          kvp_stream_t stream);
+
+/* paged_attention_decode over listed blocks: selected [num_seqs][num_kv_heads]
+ * [num_selected] holds logical block numbers in any order, negative entries
+ * are skipped, a block listed twice counts twice; query heads of KV head h
+ * attend to the tokens below context_lens[s] of the blocks in its list. A row
+ * without such a token is zero. Keys and values of slots past the context are
+ * not read. The pools are of dtype, or E4M3 (cache_dtype KVP_FP8_E4M3, with
+ * k_scale and v_scale [num_kv_heads] as in paged_attention_decode_fp8; NULL
+ * otherwise). Any num_q_heads / num_kv_heads; softmax statistics and sums are
+ * fp32.
+ * Recorded: a length outside [0, max_context_len] (clamped), a listed block
+ * past the context and a block id outside the pool (both skipped).
+ * Errors: KVP_ERR_INVALID (sizes, types, scale not finite, NULL or misaligned
+ * pointers, num_blocks * num_kv_heads * block_size of 2^31 or more). */
+KVP_API int paged_attention_decode_sparse(const void* q, const void* k_cache, const void* v_cache,
+                                          const float* k_scale, const float* v_scale,
+                                          const int32_t* block_tables, const int32_t* context_lens,
+                                          const int32_t* selected, int32_t num_seqs,
+                                          int32_t num_q_heads, int32_t num_kv_heads,
+                                          int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                          int32_t max_blocks_per_seq, int32_t max_context_len,
+                                          int32_t num_selected, float scale, void* out,
+                                          int32_t dtype, int32_t cache_dtype, kvp_stream_t stream);
 
 /* ---- virtually contiguous KV cache (CUDA virtual memory management) --------
  * The alternative the pages name to block tables: keep each sequence's cache

@@ -23,6 +23,8 @@ Modules:
 * :mod:`oracle.attention` - decode attention over a paged cache: gather each
   sequence's blocks into contiguous K/V, then softmax(q K^T * scale) V in
   fp64; plus the partition / log-sum-exp merge used for long contexts.
+* :mod:`oracle.sparse` - block-sparse decoding: rotary append, key bounds,
+  block selection, attention over listed blocks.
 * :mod:`oracle.capacity` - the KV bytes-per-token capacity model and the
   waste measures.
 * :mod:`oracle.numerics` - decoding of fp16 / bf16 bit patterns to fp64.

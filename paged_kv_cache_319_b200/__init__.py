@@ -8,7 +8,10 @@ is no Python or CPU fallback; calls fail loudly if ``libkvp.so`` is missing.
 Host side: :class:`BlockPool` (fixed-size physical blocks, per-sequence block
 tables, allocation on growth, fork with refcounted copy-on-write, release).
 Device side (torch CUDA tensors, the current torch stream):
-:func:`reshape_and_cache`, :func:`copy_blocks`, :func:`paged_attention_decode`.
+:func:`reshape_and_cache`, :func:`copy_blocks`, :func:`paged_attention_decode`;
+for decoding over a part of a long context, :func:`rope_reshape_and_cache`,
+:func:`update_key_bounds`, :func:`select_blocks`,
+:func:`paged_attention_decode_sparse`.
 """
 
 from __future__ import annotations
@@ -25,7 +28,8 @@ __all__ = [
     "paged_attention_prefill", "reshape_and_cache_fp8", "paged_attention_decode_fp8",
     "decode_workspace_bytes", "decode_grouped_workspace_bytes", "group_plan", "check_device_error",
     "VCache", "reshape_and_cache_vcache", "attention_decode_vcache", "pack_plan",
-    "paged_attention_decode_packed",
+    "paged_attention_decode_packed", "rope_reshape_and_cache", "update_key_bounds",
+    "select_blocks", "paged_attention_decode_sparse",
     "kv_bytes_per_token", "version",
     "KVP_F16", "KVP_BF16", "KVP_FP8_E4M3",
 ]
@@ -663,6 +667,196 @@ def attention_decode_vcache(q, vc: VCache, seq_slots, context_lens, scale: float
                                         context_lens.data_ptr(), S, Hq, mcl, float(scale),
                                         int(partition_size), ws_ptr, ws_bytes, out.data_ptr(),
                                         _stream(dev)))
+    return out
+
+
+def _call(dev, fn, *args) -> None:
+    """``fn(*args, stream)`` with ``dev`` current, on its current stream."""
+    cuda = _torch().cuda
+    if cuda.current_device() == dev.index:
+        check(fn(*args, _stream(dev)))
+    else:
+        with cuda.device(dev):
+            check(fn(*args, _stream(dev)))
+
+
+def _cache_code(k_cache, v_cache, dtype) -> int:
+    """Cache type of pools beside 16-bit rows of ``dtype``: theirs, or E4M3."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must both be [NB, Hkv, bs, D]")
+    if _is_e4m3(k_cache) and _is_e4m3(v_cache):
+        return KVP_FP8_E4M3
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise TypeError("the caches must have the dtype of the rows, or be E4M3")
+    return _code(k_cache)
+
+
+def _scale_ptrs(k_scale, v_scale, cache_code, Hkv, dev):
+    """Pointers of an E4M3 cache's scales; a 16-bit cache has none."""
+    if cache_code != KVP_FP8_E4M3:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale / v_scale belong to E4M3 caches")
+        return None, None
+    if k_scale is None or v_scale is None:
+        raise ValueError("an E4M3 cache needs k_scale and v_scale")
+    _fp8_scales(k_scale, v_scale, Hkv, dev)
+    return k_scale.data_ptr(), v_scale.data_ptr()
+
+
+def _rows(x, name: str, dev) -> int:
+    """Checks ``x [T, H, D]`` on ``dev`` with contiguous tokens; its token stride."""
+    if x.device != dev:
+        raise ValueError("all tensors must be on the same CUDA device")
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    if x.numel() and ((x.shape[2] > 1 and x.stride(2) != 1) or
+                      (x.shape[1] > 1 and x.stride(1) != x.shape[2])):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def _tables_lens(block_tables, context_lens, S: int, bs: int, max_context_len) -> tuple[int, int]:
+    """Checks the batch metadata; (max_blocks_per_seq, max_context_len)."""
+    torch = _torch()
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+        raise ValueError("batch metadata mismatch")
+    MB = block_tables.shape[1]
+    mcl = min(MB * bs, 2**31 - 1) if max_context_len is None else int(max_context_len)
+    if mcl > 2**31 - 1:
+        raise ValueError("max_context_len must be below 2^31")
+    return max(MB, 1), mcl
+
+
+def rope_reshape_and_cache(q, k_new, v_new, cos_sin, positions, k_cache, v_cache, slot_mapping,
+                           q_out=None, *, interleaved: bool = False, k_scale=None, v_scale=None):
+    """Rotates ``q [T, Hq, D]`` and ``k_new [T, Hkv, D]`` to their ``positions [T]`` and
+    stores keys and ``v_new`` at ``slot_mapping [T]``; returns the rotated queries.
+
+    ``cos_sin`` is CUDA float32 ``[max_positions, rot_dim]``: a position's rot_dim / 2
+    cosines, then its sines. ``interleaved`` pairs channels (2i, 2i + 1) instead of
+    (i, rot_dim / 2 + i). The rows may be strided by token (views of one projection's
+    output); ``q_out`` may be ``q`` itself. The caches are of the rows' dtype, or E4M3
+    with ``k_scale`` and ``v_scale`` as for :func:`reshape_and_cache_fp8`. A negative
+    slot stores nothing; a negative position with it leaves the row of ``q_out`` too."""
+    torch = _torch()
+    dev = _cuda(k_cache, v_cache, cos_sin, positions, slot_mapping)
+    strides = [_rows(x, n, dev) for x, n in ((q, "q"), (k_new, "k_new"), (v_new, "v_new"))]
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    strides.append(_rows(q_out, "q_out", dev))
+    if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int64:
+        raise TypeError("positions and slot_mapping must be int64")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+        raise TypeError("cos_sin must be float32 [max_positions, rot_dim]")
+    if not (q.dtype == k_new.dtype == v_new.dtype == q_out.dtype):
+        raise TypeError("dtype mismatch")
+    cache_code = _cache_code(k_cache, v_cache, q.dtype)
+    T, Hq, D = q.shape
+    NB, Hkv, bs, D2 = k_cache.shape
+    if (k_new.shape != (T, Hkv, D) or v_new.shape != k_new.shape or D2 != D or
+            q_out.shape != q.shape or positions.shape != (T,) or slot_mapping.shape != (T,)):
+        raise ValueError("shape mismatch")
+    ks, vs = _scale_ptrs(k_scale, v_scale, cache_code, Hkv, dev)
+    _call(dev, lib().rope_reshape_and_cache, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+          q_out.data_ptr(), *strides, cos_sin.data_ptr(), positions.data_ptr(), cos_sin.shape[0],
+          cos_sin.shape[1], 1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(),
+          slot_mapping.data_ptr(), ks, vs, T, Hq, Hkv, D, bs, NB, _code(q), cache_code)
+    return q_out
+
+
+def update_key_bounds(k_cache, key_bounds, block_tables, context_lens, *, new_tokens=None,
+                      max_new_tokens: int | None = None,
+                      max_context_len: int | None = None) -> None:
+    """Recomputes ``key_bounds [NB, Hkv, 2, D]``, the channel-wise largest and smallest
+    valid key of each block, for the blocks that hold one of the newest ``new_tokens[s]``
+    (CUDA int32 ``[S]``) tokens of a sequence, or for all its blocks (None).
+
+    ``max_new_tokens`` bounds the entries of ``new_tokens`` (default: the context's
+    bound). The bounds have the cache's dtype, or float16 (the codes' values) over an
+    E4M3 cache."""
+    torch = _torch()
+    dev = _cuda(k_cache, key_bounds, block_tables, context_lens)
+    code = _cache_code(k_cache, k_cache, k_cache.dtype)
+    NB, Hkv, bs, D = k_cache.shape
+    if key_bounds.shape != (NB, Hkv, 2, D):
+        raise ValueError("key_bounds must be [NB, Hkv, 2, D]")
+    if key_bounds.dtype != (torch.float16 if code == KVP_FP8_E4M3 else k_cache.dtype):
+        raise TypeError("key_bounds must have the cache's dtype (float16 over an E4M3 cache)")
+    S = block_tables.shape[0]
+    MB, mcl = _tables_lens(block_tables, context_lens, S, bs, max_context_len)
+    new_ptr = None
+    if new_tokens is not None:
+        if _cuda(new_tokens) != dev or new_tokens.dtype != torch.int32 or new_tokens.shape != (S,):
+            raise ValueError("new_tokens must be CUDA int32 [S] on the cache's device")
+        new_ptr = new_tokens.data_ptr()
+    most = mcl if max_new_tokens is None else int(max_new_tokens)
+    _call(dev, lib().update_key_bounds, k_cache.data_ptr(), key_bounds.data_ptr(),
+          block_tables.data_ptr(), context_lens.data_ptr(), new_ptr, S, Hkv, D, bs, NB, MB, mcl,
+          most, code)
+
+
+def select_blocks(q, key_bounds, block_tables, context_lens, out=None, *, block_size: int,
+                  num_selected: int, num_sink: int = 1, num_recent: int = 1,
+                  max_context_len: int | None = None):
+    """The blocks that ``q [S, Hq, D]`` needs most, per sequence and KV head; returns
+    ``out`` int32 ``[S, Hkv, num_selected]``: logical block numbers, ascending, -1 behind.
+
+    The first ``num_sink`` and last ``num_recent`` blocks are always kept, the others by an
+    upper bound on the group's logits from ``key_bounds`` (see :func:`update_key_bounds`);
+    a context of at most ``num_selected`` blocks keeps them all."""
+    torch = _torch()
+    dev = _cuda(q, key_bounds, block_tables, context_lens)
+    S, Hq, D = q.shape
+    if key_bounds.dim() != 4 or key_bounds.shape[2] != 2 or key_bounds.shape[3] != D:
+        raise ValueError("key_bounds must be [NB, Hkv, 2, D]")
+    NB, Hkv = key_bounds.shape[:2]
+    if key_bounds.dtype == q.dtype:
+        code = _code(q)
+    elif key_bounds.dtype == torch.float16:
+        code = KVP_FP8_E4M3
+    else:
+        raise TypeError("key_bounds must have q's dtype, or float16 (bounds of an E4M3 cache)")
+    MB, mcl = _tables_lens(block_tables, context_lens, S, int(block_size), max_context_len)
+    keep = int(num_selected)
+    if out is None:
+        out = torch.empty((S, Hkv, max(keep, 0)), dtype=torch.int32, device=dev)
+    elif _cuda(out) != dev or out.dtype != torch.int32 or out.shape != (S, Hkv, keep):
+        raise ValueError("out must be CUDA int32 [S, Hkv, num_selected]")
+    _call(dev, lib().select_blocks, q.data_ptr(), key_bounds.data_ptr(), block_tables.data_ptr(),
+          context_lens.data_ptr(), out.data_ptr(), S, Hq, Hkv, D, int(block_size), NB, MB, mcl,
+          keep, int(num_sink), int(num_recent), _code(q), code)
+    return out
+
+
+def paged_attention_decode_sparse(q, k_cache, v_cache, block_tables, context_lens, selected,
+                                  scale: float, out=None, *, k_scale=None, v_scale=None,
+                                  max_context_len: int | None = None):
+    """Decode attention over the blocks in ``selected`` (int32 ``[S, Hkv, n]``, as from
+    :func:`select_blocks`; any order, negative entries skipped); returns ``out [S, Hq, D]``.
+
+    The caches are of q's dtype, or E4M3 with ``k_scale`` and ``v_scale`` (CUDA float32
+    ``[Hkv]``). A row whose list leaves no token is zero."""
+    torch = _torch()
+    dev = _cuda(q, k_cache, v_cache, block_tables, context_lens, selected)
+    S, Hq, D = q.shape
+    code = _cache_code(k_cache, v_cache, q.dtype)
+    NB, Hkv, bs, D2 = k_cache.shape
+    if D2 != D:
+        raise ValueError("q / cache mismatch")
+    if selected.dtype != torch.int32 or selected.dim() != 3 or selected.shape[:2] != (S, Hkv):
+        raise ValueError("selected must be int32 [S, Hkv, n]")
+    MB, mcl = _tables_lens(block_tables, context_lens, S, bs, max_context_len)
+    ks, vs = _scale_ptrs(k_scale, v_scale, code, Hkv, dev)
+    if out is None:
+        out = torch.empty_like(q)
+    elif _cuda(out) != dev or out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out mismatch")
+    _call(dev, lib().paged_attention_decode_sparse, q.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), ks, vs, block_tables.data_ptr(), context_lens.data_ptr(),
+          selected.data_ptr(), S, Hq, Hkv, D, bs, NB, MB, mcl, selected.shape[2], float(scale),
+          out.data_ptr(), _code(q), code)
     return out
 
 

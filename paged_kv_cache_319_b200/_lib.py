@@ -117,6 +117,15 @@ SIGNATURES = {
     "kvp_decode_packed_workspace_bytes": (sz, [P_i32, i32, i32, i32]),
     "paged_attention_decode_packed": (C.c_int, [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32,
                                                 f32, P_i32, vp, vp, sz, vp, i32, vp]),
+    "rope_reshape_and_cache": (C.c_int, [vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, i64, i32, i32,
+                                         vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32,
+                                         i32, vp]),
+    "update_key_bounds": (C.c_int, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32,
+                                    i32, vp]),
+    "select_blocks": (C.c_int, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32,
+                                i32, i32, i32, i32, vp]),
+    "paged_attention_decode_sparse": (C.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32,
+                                                i32, i32, i32, i32, i32, f32, vp, i32, i32, vp]),
     "kvp_check_device_error": (C.c_int, [vp]),
     "kvp_selftest_bounded_wait": (C.c_int, [i32, vp]),
     "kvp_last_error_message": (C.c_char_p, []),

@@ -8,6 +8,7 @@ tree; intermediate output (the ptxas report) goes to ``_build/``.
 from __future__ import annotations
 
 import argparse
+import concurrent.futures
 import os
 import shutil
 import subprocess
@@ -25,6 +26,7 @@ SOURCES = [
     os.path.join(CSRC, "host", "group_plan.cpp"),
     os.path.join(CSRC, "host", "vcache.cpp"),
     os.path.join(CSRC, "kvp_device.cu"),
+    os.path.join(CSRC, "kvp_sparse.cu"),
 ]
 
 
@@ -56,23 +58,32 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
     tmp = LIB + ".tmp"
-    cmd = [
-        nvcc(), "-std=c++17", "-O3", "-lineinfo", "-DNDEBUG",
+    flags = [
+        "-std=c++17", "-O3", "-lineinfo", "-DNDEBUG",
         "-gencode", "arch=compute_100a,code=sm_100a",
         "-Xcompiler", "-fPIC,-O3,-fvisibility=hidden",
         "-Xptxas", "-v",
         "-I", INCLUDE, "-I", CSRC,
-        "-shared", "-o", tmp,
-    ] + SOURCES
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    ]
+    # one object per source, compiled side by side (kvp_device.cu takes minutes)
+    objects = [os.path.join(BUILD_DIR, os.path.basename(src) + ".o") for src in SOURCES]
+    jobs = [[nvcc()] + flags + ["-c", src, "-o", obj] for src, obj in zip(SOURCES, objects)]
+    with concurrent.futures.ThreadPoolExecutor(len(jobs)) as pool:
+        done = list(pool.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
+    cmds, out = jobs, "".join(r.stdout + r.stderr for r in done)
+    failed = any(r.returncode for r in done)
+    if not failed:
+        link = [nvcc()] + flags + ["-shared", "-o", tmp] + objects
+        res = subprocess.run(link, capture_output=True, text=True)
+        cmds, out, failed = cmds + [link], out + res.stdout + res.stderr, res.returncode != 0
     with open(os.path.join(BUILD_DIR, "nvcc.log"), "w") as f:
-        f.write(" ".join(cmd) + "\n\n" + res.stdout + res.stderr)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
+        f.write("\n".join(" ".join(c) for c in cmds) + "\n\n" + out)
+    if failed:
+        sys.stderr.write(out)
         raise RuntimeError("nvcc failed; see " + os.path.join(BUILD_DIR, "nvcc.log"))
     os.replace(tmp, LIB)
     if verbose:
-        sys.stdout.write(res.stdout + res.stderr)
+        sys.stdout.write(out)
     return LIB
 
 

@@ -1,8 +1,8 @@
 // Device entry points of libkvp (C ABI): argument checks, TMA tensor maps,
 // kernel selection by geometry, launches on the caller's stream.
 //
-// All device code lives in this one translation unit (the kernels are
-// headers) so the device error word is a single symbol per GPU.
+// The kernels are headers; those of block-sparse decoding are compiled by
+// kvp_sparse.cu, which has a device error word of its own.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -23,11 +23,11 @@
 #include "kernels/decode_simt.cuh"
 #include "kernels/decode_tc.cuh"
 #include "kernels/prefill_tc.cuh"
+#include "launch_util.h"
 #include "pack_layout.h"
+#include "sparse.h"
 #include "status.h"
 #include "vcache.h"
-
-using kvp::fail;
 
 // Launch shape of the CUDA-core decode kernel: warps per CTA and TMA stages per
 // warp (shared memory per CTA = warps x stages x 2 tiles + merge area). The
@@ -83,52 +83,6 @@ using kvp::fail;
 #endif
 
 namespace {
-
-constexpr int kMaxDevices = 64;
-
-int cuda_fail(cudaError_t e, const char* what) {
-  return fail(KVP_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-int current_device() {
-  int d = 0;
-  cudaGetDevice(&d);
-  return d;
-}
-
-int sm_count() {
-  static std::atomic<int> cache[kMaxDevices];
-  const int d = current_device();
-  if (d < 0 || d >= kMaxDevices) return 148;
-  int n = cache[d].load(std::memory_order_relaxed);
-  if (n == 0) {
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d);
-    if (n <= 0) n = 148;
-    cache[d].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
-// Raises a kernel's dynamic shared-memory limit once per (kernel, device).
-template <typename K>
-cudaError_t ensure_smem(K kernel, int bytes) {
-  static std::mutex mu;
-  static std::unordered_map<const void*, uint64_t> done;  // kernel -> device bit mask
-  const int d = current_device();
-  const uint64_t bit = d < 64 ? (1ull << d) : 0;
-  const void* key = reinterpret_cast<const void*>(kernel);
-  {
-    std::lock_guard<std::mutex> g(mu);
-    auto it = done.find(key);
-    if (bit && it != done.end() && (it->second & bit)) return cudaSuccess;
-  }
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && bit) {
-    std::lock_guard<std::mutex> g(mu);
-    done[key] |= bit;
-  }
-  return e;
-}
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -260,14 +214,6 @@ int make_map_prefill_q(CUtensorMap* map, const void* base, int32_t dtype, uint32
 #ifndef KVP_VCACHE_SIMT_TILE
 #define KVP_VCACHE_SIMT_TILE 16
 #endif
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-int ilog2(int64_t v) {
-  int l = 0;
-  while ((int64_t(1) << l) < v) ++l;
-  return (int64_t(1) << l) == v ? l : -1;
-}
 
 struct Workspace {
   size_t ml_bytes, acc_bytes, total;
@@ -1555,17 +1501,26 @@ int kvp_check_device_error(kvp_stream_t stream) {
   unsigned long long v = 0;
   e = cudaMemcpyFromSymbol(&v, kvp::dev::g_error_word, sizeof(v));
   if (e != cudaSuccess) return cuda_fail(e, "kvp_check_device_error: read");
-  if (v == 0) return KVP_OK;
-  const unsigned long long zero = 0;
-  e = cudaMemcpyToSymbol(kvp::dev::g_error_word, &zero, sizeof(zero));
-  if (e != cudaSuccess) return cuda_fail(e, "kvp_check_device_error: clear");
+  unsigned long long v2 = 0;  // the word of kvp_sparse.cu, cleared by this call
+  const int rc = kvp_sparse_take_error(&v2);
+  if (rc) return rc;
+  if (v == 0 && v2 == 0) return KVP_OK;
+  if (v) {
+    const unsigned long long zero = 0;
+    e = cudaMemcpyToSymbol(kvp::dev::g_error_word, &zero, sizeof(zero));
+    if (e != cudaSuccess) return cuda_fail(e, "kvp_check_device_error: clear");
+  } else {
+    v = v2;
+  }
   const unsigned kind = unsigned(v >> 56);
   const unsigned long long payload = v & ((1ull << 56) - 1);
   static const char* names[] = {"none", "slot out of range (token index)",
                                 "block table entry out of range (seq << 32 | logical block)",
                                 "context length out of range (sequence)",
-                                "copy pair out of range (pair index)", "bounded wait timed out (site)"};
-  const char* name = kind < 6 ? names[kind] : "unknown";
+                                "copy pair out of range (pair index)", "bounded wait timed out (site)",
+                                "position out of range (token index)",
+                                "selected block past the context (list << 32 | logical block)"};
+  const char* name = kind < 8 ? names[kind] : "unknown";
   if (kind == kvp::dev::KVP_DEVERR_TIMEOUT)
     return fail(KVP_ERR_CUDA, "device: %s 0x%llx", name, payload);
   return fail(KVP_ERR_BOUNDS, "device: %s %llu", name, payload);
