@@ -10,21 +10,23 @@
 //
 // Bound by HBM: a listed block's keys and values are read once per KV head and
 // serve the whole group. Every warp works alone on tiles of 16 tokens (two
-// half tiles of 8, so blocks of 8, 16 and 32 tokens are alike) that it loads
-// from global memory straight into mma.sync operand registers: 8 KiB in flight
-// per warp with no shared-memory round trip and no barrier, so occupancy alone
-// covers the latency of the scattered reads. Keys and values are the A operand
-// (16 tokens, or 16 channels, by 16) and up to 8 query heads per column tile the
-// B operand: at the 2 to 32 FLOP per byte of this operator the legacy
-// tensor-core path is nowhere near its limit, and a tcgen05 tile would need
-// 128 rows staged in shared memory first.
+// half tiles of 8, so blocks of 8, 16 and 32 tokens are alike): bulk copies
+// (cp.async.bulk; a block's rows of one head are contiguous) fill a ring of
+// stages of its own, and mma.sync multiplies from there. Keys and values are
+// the A operand (16 tokens, or 16 channels, by 16) and up to 8 query heads per
+// column tile the B operand: at the 2 to 32 FLOP per byte of this operator the
+// legacy tensor-core path is nowhere near its limit (12% busy), and a tcgen05
+// tile would need 128 rows staged in shared memory first. What bounds a warp is
+// the latency of its chain of instructions per tile, so the softmax takes one
+// vote per tile and no reduction (32 sequences x 32 heads x 4096 tokens, bf16:
+// 125 us with a reduction and a rescaling per tile, 105 us without).
 //
 // Operand layout. In m16n8k16, lane l holds rows l/4 and l/4 + 8 of A and, of
 // each row, the k positions 2p, 2p+1, 2p+8, 2p+9 (p = l % 4). A contraction may
 // take its k positions in any order if both operands agree:
-//  - logits (k = channels): lane l loads 16 contiguous bytes of its token rows,
-//    so a 16-byte load feeds two (E4M3: four) k steps; queries are loaded alike.
-//  - output (rows = channels, k = tokens): lane l loads 16 bytes of channels
+//  - logits (k = channels): lane l reads 16 contiguous bytes of its token rows,
+//    so a 16-byte read feeds two (E4M3: four) k steps; queries are loaded alike.
+//  - output (rows = channels, k = tokens): lane l reads 16 bytes of channels
 //    of tokens 2p, 2p+1, 2p+8, 2p+9 and pairs neighbouring tokens' values with
 //    byte permutes; row l/4 of the row tiles stands for the lane's channels.
 // The probabilities come out of the first product as [token][head] and enter
@@ -60,6 +62,15 @@ struct SparseArgs {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kChunk = 512;  // tiles located per pass over the list
+
+// Shared memory: per warp kStageBytes of K/V stages (later the merge area), then
+// the located rows and valid tokens of kChunk tiles' halves, then the barriers.
+// Two stages of 8 KiB (D = 128, 16-bit) or four of 4 KiB and three CTAs per SM:
+// a CTA's start and merge are covered by its neighbours' loads (64 sequences x 40
+// heads x 512 tokens: 108 us; two CTAs with three stages 124, one with six 182).
+constexpr int kStageBytes = 16 * 1024;
+constexpr int kSmemBytes = kWarps * kStageBytes + kChunk * 10 + kWarps * 16 * 8;
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -87,13 +98,29 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// 16 bytes that are read once.
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
+// Contiguous copy of `bytes` (a multiple of 16) into shared memory; completes
+// bar's transaction count. Addresses are 16-byte aligned.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 x;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-               : "l"(p));
+               : "r"(addr));
   return x;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ uint32_t word(const uint4& x, int i) {
@@ -102,7 +129,7 @@ __device__ __forceinline__ uint32_t word(const uint4& x, int i) {
 
 // T: queries, output and products; FP8: E4M3 cache (D = 128); NT: tiles of 8 heads.
 template <typename T, bool FP8, int D, int NT>
-__global__ void __launch_bounds__(kThreads) decode_sparse_kernel(const SparseArgs a) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) decode_sparse_kernel(const SparseArgs a) {
   namespace cg = cooperative_groups;
   constexpr int ROW = D * (FP8 ? 1 : 2);  // bytes of a cached row
   constexpr int KL = ROW / 64;            // 16-byte key loads per token row and lane
@@ -110,14 +137,26 @@ __global__ void __launch_bounds__(kThreads) decode_sparse_kernel(const SparseArg
   constexpr int MT = D / 16;              // 16-channel row tiles of the output
   constexpr int QW = D / 8;               // query words per lane and head tile
   constexpr int HEADS = NT * 8;
+  // type of the products: E4M3 values are fp16 values, so an E4M3 cache takes fp16
+  // products (bf16 queries scaled by a power of two into its range)
+  using M = typename std::conditional<FP8, __half, T>::type;
+  constexpr bool kScaleQ = FP8 && !std::is_same<T, __half>::value;
   static_assert(!FP8 || D == 128, "E4M3 caches have head_dim 128");
 
-  extern __shared__ float sm[];
-  float* sm_acc = sm;                                 // [kWarps][HEADS][D]
-  float* sm_m = sm + kWarps * HEADS * D;              // [kWarps][HEADS]
+  constexpr int TILE = 16 * ROW;                    // bytes of a tile's keys
+  constexpr int STAGES = kStageBytes / (2 * TILE);
+  static_assert(STAGES <= 16 && kWarps * kStageBytes >= (kWarps * HEADS * (D + 2) + 2 * HEADS) * 4,
+                "the merge area lies over the stages");
+
+  extern __shared__ __align__(128) unsigned char smem[];
+  float* sm_acc = reinterpret_cast<float*>(smem);     // [kWarps][HEADS][D]
+  float* sm_m = sm_acc + kWarps * HEADS * D;          // [kWarps][HEADS]
   float* sm_l = sm_m + kWarps * HEADS;
   float* part_m = sm_l + kWarps * HEADS;              // [HEADS], this CTA's merged partial
   float* part_l = part_m + HEADS;
+  uint2* rows = reinterpret_cast<uint2*>(smem + kWarps * kStageBytes);  // [kChunk], a row per half
+  uint16_t* valid = reinterpret_cast<uint16_t*>(rows + kChunk);         // [kChunk], a byte per half
+  uint64_t* bars = reinterpret_cast<uint64_t*>(valid + kChunk);         // [kWarps][16]
 
   cg::cluster_group cluster = cg::this_cluster();
   const uint32_t nranks = cluster.num_blocks(), rank = cluster.block_rank();
@@ -154,9 +193,33 @@ __global__ void __launch_bounds__(kThreads) decode_sparse_kernel(const SparseArg
       qf[t][4 * i] = x.x, qf[t][4 * i + 1] = x.y, qf[t][4 * i + 2] = x.z, qf[t][4 * i + 3] = x.w;
     }
   }
-  const float scale = FP8 ? a.scale_log2 * __ldg(a.k_scale + g) : a.scale_log2;
+  float scale[NT][2];  // of the logits of columns 2p, 2p + 1
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    scale[t][0] = scale[t][1] = FP8 ? a.scale_log2 * __ldg(a.k_scale + g) : a.scale_log2;
+    if constexpr (kScaleQ) {
+      // each head's queries times 2^k with the largest in [2^14, 2^15): what is
+      // lost below fp16's normal range is 2^-39 of the largest or less
+      uint32_t big = 0;
+#pragma unroll
+      for (int i = 0; i < QW; ++i) big = __vmaxu2(big, qf[t][i] & 0x7fff7fffu);
+      big = max(big >> 16, big & 0xffffu);
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      const uint32_t e = min(268u - (big >> 7), 253u);  // biased exponent of 2^k
+      const float up = __uint_as_float(e << 23), down = __uint_as_float((254u - e) << 23);
+#pragma unroll
+      for (int i = 0; i < QW; ++i) {
+        const float2 f = Elem<T>::to_float2(qf[t][i]);
+        qf[t][i] = Elem<M>::pack2(f.x * up, f.y * up);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) scale[t][c] *= __shfl_sync(0xffffffffu, down, (2 * p + c) * 4);
+    }
+  }
 
   float acc[NT][MT][4];
+  // m: the reference of the exponentials, a recent maximum; l: this lane's sum
   float m[NT][2], l[NT][2];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -172,7 +235,8 @@ __global__ void __launch_bounds__(kThreads) decode_sparse_kernel(const SparseArg
   const int32_t* table = a.block_tables + int64_t(s) * a.max_blocks_per_seq;
   const int halves = a.num_selected << (a.log2_bs - 3);  // half tiles of 8 tokens
   const int tiles = (halves + 1) >> 1;
-  const int stride = int(nranks) * kWarps, w0 = int(rank) * kWarps + wid;
+  // tile j of this CTA is tile ((j / kWarps) * nranks + rank) * kWarps + j % kWarps of the list
+  const int rounds = (tiles + kWarps * int(nranks) - 1) / (kWarps * int(nranks));
 
   // cache row (block, head, slot) of half tile `half`, and its tokens below ctx
   auto locate = [&](int half, uint32_t& row, int& valid) {
@@ -195,64 +259,103 @@ __global__ void __launch_bounds__(kThreads) decode_sparse_kernel(const SparseArg
     valid = max(0, min(8, ctx - (lb << a.log2_bs) - off));
   };
 
-  for (int base = w0; base < tiles; base += 32 * stride) {
-    // lane i locates the warp's i-th tile of the next 32
-    uint32_t row0 = 0, row1 = 0;
-    int v0 = 0, v1 = 0;
-    {
-      const int t = base + lane * stride;
-      if (t < tiles) {
-        locate(2 * t, row0, v0);
-        locate(2 * t + 1, row1, v1);
-      }
+  uint64_t* bar = bars + wid * 16;
+  if (lane < STAGES) mbar_init(bar + lane, 1);
+  fence_mbar_init();
+  const uint32_t stage0 = smem_u32(smem) + wid * kStageBytes;
+  const uint64_t policy = l2_policy_evict_first();
+  uint32_t phases = 0;  // parity of each stage's next completion
+  bool alive = true;
+
+  for (int j0 = 0; j0 < rounds * kWarps; j0 += kChunk) {
+    const int here = min(kChunk, rounds * kWarps - j0);
+    for (int j = tid; j < here; j += kThreads) {
+      const int t = (((j0 + j) / kWarps) * int(nranks) + int(rank)) * kWarps + j % kWarps;
+      uint2 row;
+      int va, vb;
+      locate(2 * t, row.x, va);
+      locate(2 * t + 1, row.y, vb);
+      rows[j] = row;
+      valid[j] = uint16_t(va | (vb << 8));
     }
-    const int batch = min(32, (tiles - base + stride - 1) / stride);
-    for (int i = 0; i < batch; ++i) {
-      const uint32_t ra = __shfl_sync(0xffffffffu, row0, i), rb = __shfl_sync(0xffffffffu, row1, i);
-      const int va = __shfl_sync(0xffffffffu, v0, i), vb = __shfl_sync(0xffffffffu, v1, i);
-      if (va + vb == 0) continue;
+    __syncthreads();
+    const int mine = here / kWarps;
+    // loads of the warp's tile i into stage st; rows past the context are never read
+    auto issue = [&](int i, int st) {
+      const int j = i * kWarps + wid;
+      const uint32_t v = valid[j], va = v & 0xffu, vb = v >> 8;
+      if (v == 0) return;
+      if (lane == 0) mbar_arrive_expect_tx(bar + st, (va + vb) * 2 * ROW);
+      __syncwarp();
+      if (lane < 4) {  // lane bit 0: half tile, bit 1: keys or values
+        const uint2 row = rows[j];
+        const bool one = va == 8 && row.y == row.x + 8;  // neighbours: one copy
+        const uint32_t half = lane & 1;
+        const uint32_t n = half ? (one ? 0 : vb) : (one ? 8 + vb : va);
+        const char* src = static_cast<const char*>(lane >> 1 ? a.v_cache : a.k_cache);
+        if (n)
+          bulk_load(stage0 + st * 2 * TILE + (lane >> 1) * TILE + half * (TILE / 2),
+                    src + int64_t(half ? row.y : row.x) * ROW, n * ROW, bar + st, policy);
+      }
+    };
+    if (alive)
+      for (int i = 0; i < min(mine, STAGES - 1); ++i) issue(i, i);
+    int st = -1, fill = STAGES - 2;  // stages of tile i and of tile i + STAGES - 1
+    for (int i = 0; i < mine && alive; ++i) {
+      st = st + 1 == STAGES ? 0 : st + 1;
+      fill = fill + 1 == STAGES ? 0 : fill + 1;
+      __syncwarp();  // every lane has read the stage that is filled next
+      if (i + STAGES - 1 < mine) issue(i + STAGES - 1, fill);
+      const int v = valid[i * kWarps + wid], va = v & 0xff, vb = v >> 8;
+      if (v == 0) continue;
+      const bool ok = mbar_wait(bar + st, (phases >> st) & 1u, 0x5000u + st);
+      phases ^= 1u << st;
+      if (!__all_sync(0xffffffffu, ok)) {
+        // give up: wait (each with the limit) for the copies in flight, read nothing
+        for (int k = i + 1; k < min(mine, i + STAGES); ++k)
+          if (valid[k * kWarps + wid])
+            mbar_wait(bar + k % STAGES, (phases >> (k % STAGES)) & 1u, 0x5000u + st);
+        alive = false;
+        break;
+      }
 
-      // ---- loads; rows past the context are zeros, never read ----
       uint4 kx[2][KL], vx[4][VL];
-      const char* kc = static_cast<const char*>(a.k_cache);
-      const char* vc = static_cast<const char*>(a.v_cache);
+      const uint32_t ks = stage0 + st * 2 * TILE, vs = ks + TILE;
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const bool ok = r < (y ? vb : va);
-        const char* src = kc + int64_t((y ? rb : ra) + r) * ROW + p * 16;
+      for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int j = 0; j < KL; ++j) {
-          kx[y][j] = make_uint4(0, 0, 0, 0);
-          if (ok) kx[y][j] = ld_stream(src + j * 64);
-        }
-      }
+        for (int j = 0; j < KL; ++j) kx[y][j] = lds128(ks + (y * 8 + r) * ROW + p * 16 + j * 64);
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int tok = 2 * p + (y & 1);
-        const bool ok = tok < (y >> 1 ? vb : va);
-        const char* src = vc + int64_t((y >> 1 ? rb : ra) + tok) * ROW + r * 16;
+      for (int y = 0; y < 4; ++y)
 #pragma unroll
-        for (int j = 0; j < VL; ++j) {
-          vx[y][j] = make_uint4(0, 0, 0, 0);
-          if (ok) vx[y][j] = ld_stream(src + j * 128);
-        }
+        for (int j = 0; j < VL; ++j)
+          vx[y][j] = lds128(vs + ((y >> 1) * 8 + 2 * p + (y & 1)) * ROW + r * 16 + j * 128);
+      const bool partial = va + vb < 16;
+      if (partial) {  // a stage's unfilled value rows hold anything
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (2 * p + (y & 1) >= (y >> 1 ? vb : va))
+#pragma unroll
+            for (int j = 0; j < VL; ++j) vx[y][j] = make_uint4(0, 0, 0, 0);
       }
 
-      // ---- logits: [16 tokens][8 heads] per head tile ----
-      float z[NT][4];
+      // ---- logits: [16 tokens][8 heads] per head tile, in two chains ----
+      float z[NT][4], z1[NT][4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) z[t][0] = z[t][1] = z[t][2] = z[t][3] = 0.f;
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[t][e] = z1[t][e] = 0.f;
 #pragma unroll
       for (int j = 0; j < KL; ++j) {
         if constexpr (FP8) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {  // word c: 4 channels, one k step
             const uint32_t x = word(kx[0][j], c), y = word(kx[1][j], c);
-            const uint32_t af[4] = {e4m3x2_to_x2<T>(x & 0xffffu), e4m3x2_to_x2<T>(y & 0xffffu),
-                                    e4m3x2_to_x2<T>(x >> 16), e4m3x2_to_x2<T>(y >> 16)};
+            const uint32_t af[4] = {e4m3x2_to_x2<M>(x & 0xffffu), e4m3x2_to_x2<M>(y & 0xffffu),
+                                    e4m3x2_to_x2<M>(x >> 16), e4m3x2_to_x2<M>(y >> 16)};
 #pragma unroll
             for (int t = 0; t < NT; ++t)
-              mma16816<T>(z[t], af, qf[t][j * 8 + 2 * c], qf[t][j * 8 + 2 * c + 1]);
+              mma16816<M>(c & 1 ? z1[t] : z[t], af, qf[t][j * 8 + 2 * c], qf[t][j * 8 + 2 * c + 1]);
           }
         } else {
 #pragma unroll
@@ -261,43 +364,61 @@ __global__ void __launch_bounds__(kThreads) decode_sparse_kernel(const SparseArg
                                     word(kx[0][j], 2 * c + 1), word(kx[1][j], 2 * c + 1)};
 #pragma unroll
             for (int t = 0; t < NT; ++t)
-              mma16816<T>(z[t], af, qf[t][j * 4 + 2 * c], qf[t][j * 4 + 2 * c + 1]);
+              mma16816<M>(c ? z1[t] : z[t], af, qf[t][j * 4 + 2 * c], qf[t][j * 4 + 2 * c + 1]);
           }
         }
       }
 
-      // ---- online softmax over the tile's tokens, per head (columns 2p, 2p + 1) ----
+      // ---- online softmax, per head (columns 2p, 2p + 1; rows r and r + 8) ----
+      // The reference of the exponentials follows the maximum only when a logit
+      // exceeds it by more than 8 (a factor 256, far inside fp16's range): one
+      // vote per tile instead of a reduction over the lanes and a rescaling.
+      bool rise = false;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          z[t][e] = (z[t][e] + z1[t][e]) * scale[t][e & 1];
+          if (partial && r >= (e >> 1 ? vb : va)) z[t][e] = -INFINITY;
+          rise |= z[t][e] > m[t][e & 1] + 8.f;
+        }
+      }
+      if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float mx = fmaxf(z[t][c], z[t][2 + c]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mn = fmaxf(m[t][c], mx);
+            const float alpha = mn == -INFINITY ? 1.f : ex2(m[t][c] - mn);
+            m[t][c] = mn;
+            l[t][c] *= alpha;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) acc[t][j][c] *= alpha, acc[t][j][2 + c] *= alpha;
+          }
+      }
       uint32_t pb[NT][2], pl[NT][2];  // probabilities as the B operand, and their low parts
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float pr[4];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float x = r < va ? z[t][c] * scale : -INFINITY;
-          const float y = r < vb ? z[t][2 + c] * scale : -INFINITY;
-          float mx = fmaxf(x, y);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float mn = fmaxf(m[t][c], mx);
-          const float ms = mn == -INFINITY ? 0.f : mn;
-          const float alpha = exp2f(m[t][c] - ms);
-          pr[c] = r < va ? exp2f(x - ms) : 0.f;
-          pr[2 + c] = r < vb ? exp2f(y - ms) : 0.f;
-          m[t][c] = mn;
-          l[t][c] = l[t][c] * alpha + pr[c] + pr[2 + c];
-#pragma unroll
-          for (int j = 0; j < MT; ++j) acc[t][j][c] *= alpha, acc[t][j][2 + c] *= alpha;
+        for (int e = 0; e < 4; ++e) {
+          const float ref = m[t][e & 1];
+          pr[e] = ex2(z[t][e] - (ref == -INFINITY ? 0.f : ref));
+          l[t][e & 1] += pr[e];
         }
         // one rounding of p to 11 bits for fp16; bf16's 8 bits would cost more
         // than the output's own rounding, so p goes as a high and a low part
-        const uint32_t hi0 = Elem<T>::pack2(pr[0], pr[1]), hi1 = Elem<T>::pack2(pr[2], pr[3]);
+        const uint32_t hi0 = Elem<M>::pack2(pr[0], pr[1]), hi1 = Elem<M>::pack2(pr[2], pr[3]);
         pb[t][0] = transpose8x8(hi0);
         pb[t][1] = transpose8x8(hi1);
-        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-          const float2 f0 = Elem<T>::to_float2(hi0), f1 = Elem<T>::to_float2(hi1);
-          pl[t][0] = transpose8x8(Elem<T>::pack2(pr[0] - f0.x, pr[1] - f0.y));
-          pl[t][1] = transpose8x8(Elem<T>::pack2(pr[2] - f1.x, pr[3] - f1.y));
+        if constexpr (std::is_same<M, __nv_bfloat16>::value) {
+          const float2 f0 = Elem<M>::to_float2(hi0), f1 = Elem<M>::to_float2(hi1);
+          pl[t][0] = transpose8x8(Elem<M>::pack2(pr[0] - f0.x, pr[1] - f0.y));
+          pl[t][1] = transpose8x8(Elem<M>::pack2(pr[2] - f1.x, pr[3] - f1.y));
         }
       }
 
@@ -310,8 +431,8 @@ __global__ void __launch_bounds__(kThreads) decode_sparse_kernel(const SparseArg
           const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
           const uint32_t x = __byte_perm(word(vx[0][0], j / 2), word(vx[1][0], j / 2), sel);
           const uint32_t y = __byte_perm(word(vx[2][0], j / 2), word(vx[3][0], j / 2), sel);
-          af[0] = e4m3x2_to_x2<T>(x & 0xffffu), af[1] = e4m3x2_to_x2<T>(x >> 16);
-          af[2] = e4m3x2_to_x2<T>(y & 0xffffu), af[3] = e4m3x2_to_x2<T>(y >> 16);
+          af[0] = e4m3x2_to_x2<M>(x & 0xffffu), af[1] = e4m3x2_to_x2<M>(x >> 16);
+          af[2] = e4m3x2_to_x2<M>(y & 0xffffu), af[3] = e4m3x2_to_x2<M>(y >> 16);
         } else {
           // row tile j: channels (j/4)*64 + r*8 + 2(j%4), +1: word j%4 of load j/4
           const uint32_t x0 = word(vx[0][j / 4], j % 4), x1 = word(vx[1][j / 4], j % 4);
@@ -321,12 +442,13 @@ __global__ void __launch_bounds__(kThreads) decode_sparse_kernel(const SparseArg
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          mma16816<T>(acc[t][j], af, pb[t][0], pb[t][1]);
-          if constexpr (std::is_same<T, __nv_bfloat16>::value)
-            mma16816<T>(acc[t][j], af, pl[t][0], pl[t][1]);
+          mma16816<M>(acc[t][j], af, pb[t][0], pb[t][1]);
+          if constexpr (std::is_same<M, __nv_bfloat16>::value)
+            mma16816<M>(acc[t][j], af, pl[t][0], pl[t][1]);
         }
       }
     }
+    __syncthreads();  // the located rows, or the stages, are written next
   }
 
   // ---- merge: lanes of a column, warps, CTAs ----

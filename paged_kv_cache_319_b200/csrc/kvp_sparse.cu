@@ -131,9 +131,8 @@ int launch_sparse_nt(kvp::dev::sparse::SparseArgs a, cudaStream_t st) {
   // more CTAs per row while the rows alone leave SMs idle and each warp still has 2 tiles
   int ranks = 1;
   while (ranks < 8 && units * ranks < 4 * sm_count() && tiles >= 4 * kWarps * ranks) ranks *= 2;
-  const int smem = (kWarps * NT * 8 * (D + 2) + 2 * NT * 8) * 4;
   return launch_clusters("paged_attention_decode_sparse", decode_sparse_kernel<T, FP8, D, NT>,
-                         units, ranks, kThreads, smem, smem, a, st);
+                         units, ranks, kThreads, kSmemBytes, kSmemBytes, a, st);
 }
 
 template <typename T, bool FP8, int D>
