@@ -17,11 +17,13 @@ for decoding over a part of a long context, :func:`rope_reshape_and_cache`,
 from __future__ import annotations
 
 import ctypes as C
+import struct
 
 import numpy as np
 
-from ._lib import (KVP_BF16, KVP_F16, KVP_FP8_E4M3, KvpError, P_i32, P_i64, PoolStats,
-                   VCacheStats, check, lib)
+from ._lib import (KVP_BF16, KVP_CALL_DECODE_SPARSE, KVP_CALL_ROPE_RESHAPE_AND_CACHE,
+                   KVP_CALL_SELECT_BLOCKS, KVP_CALL_UPDATE_KEY_BOUNDS, KVP_F16, KVP_FP8_E4M3,
+                   KvpError, P_i32, P_i64, PoolStats, VCacheStats, check, lib)
 
 __all__ = [
     "BlockPool", "KvpError", "reshape_and_cache", "copy_blocks", "paged_attention_decode",
@@ -670,63 +672,87 @@ def attention_decode_vcache(q, vc: VCache, seq_slots, context_lens, scale: float
     return out
 
 
-def _call(dev, fn, *args) -> None:
-    """``fn(*args, stream)`` with ``dev`` current, on its current stream."""
-    cuda = _torch().cuda
-    if cuda.current_device() == dev.index:
-        check(fn(*args, _stream(dev)))
+# The calls below take their arguments in one block (``kvp_call_words``): per argument
+# that is a fraction of what ctypes takes, and these calls run once per layer and step.
+_ROPE, _BOUNDS, _SELECT, _SPARSE = (struct.Struct(f) for f in ("27q", "15q", "19q", "17qd4q"))
+
+
+def _index(*ts) -> int:
+    """The index of the CUDA device that all of ``ts``, contiguous, are on."""
+    idx = ts[0].get_device()
+    for t in ts:
+        if t.get_device() != idx or not t.is_contiguous():
+            _cuda(*ts)
+    if idx < 0:
+        _cuda(*ts)
+    return idx
+
+
+def _call(idx: int, call: int, words: struct.Struct, *args) -> None:
+    """Entry point ``call`` with ``args`` and the current stream of device ``idx``, with
+    that device current."""
+    torch = _torch()
+    if torch.cuda.current_device() == idx:
+        stream = torch._C._cuda_getCurrentRawStream(idx)
+        check(lib().kvp_call_words(call, words.pack(*args, stream), len(args) + 1))
     else:
-        with cuda.device(dev):
-            check(fn(*args, _stream(dev)))
+        with torch.cuda.device(idx):
+            stream = torch._C._cuda_getCurrentRawStream(idx)
+            check(lib().kvp_call_words(call, words.pack(*args, stream), len(args) + 1))
 
 
 def _cache_code(k_cache, v_cache, dtype) -> int:
     """Cache type of pools beside 16-bit rows of ``dtype``: theirs, or E4M3."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must both be [NB, Hkv, bs, D]")
-    if _is_e4m3(k_cache) and _is_e4m3(v_cache):
-        return KVP_FP8_E4M3
-    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+    kt = k_cache.dtype
+    if kt != v_cache.dtype:
+        raise TypeError("the caches must share a dtype")
+    if kt == dtype:
+        return _code(k_cache)
+    if not _is_e4m3(k_cache):
         raise TypeError("the caches must have the dtype of the rows, or be E4M3")
-    return _code(k_cache)
+    return KVP_FP8_E4M3
 
 
-def _scale_ptrs(k_scale, v_scale, cache_code, Hkv, dev):
+def _scale_ptrs(k_scale, v_scale, cache_code, Hkv, idx):
     """Pointers of an E4M3 cache's scales; a 16-bit cache has none."""
     if cache_code != KVP_FP8_E4M3:
         if k_scale is not None or v_scale is not None:
             raise ValueError("k_scale / v_scale belong to E4M3 caches")
-        return None, None
+        return 0, 0
     if k_scale is None or v_scale is None:
         raise ValueError("an E4M3 cache needs k_scale and v_scale")
-    _fp8_scales(k_scale, v_scale, Hkv, dev)
+    f32 = _torch().float32
+    if (k_scale.dtype != f32 or v_scale.dtype != f32 or k_scale.shape != (Hkv,) or
+            v_scale.shape != (Hkv,) or _index(k_scale, v_scale) != idx):
+        raise ValueError("k_scale / v_scale must be CUDA float32 [num_kv_heads] on the cache's device")
     return k_scale.data_ptr(), v_scale.data_ptr()
 
 
-def _rows(x, name: str, dev) -> int:
-    """Checks ``x [T, H, D]`` on ``dev`` with contiguous tokens; its token stride."""
-    if x.device != dev:
+def _rows(x, name: str, idx: int, T: int, D: int) -> tuple[int, int]:
+    """Checks ``x [T, heads, D]`` on device ``idx``, each token's heads contiguous;
+    (heads, elements between tokens)."""
+    if x.get_device() != idx:
         raise ValueError("all tensors must be on the same CUDA device")
     if x.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    if x.numel() and ((x.shape[2] > 1 and x.stride(2) != 1) or
-                      (x.shape[1] > 1 and x.stride(1) != x.shape[2])):
+    T2, H, D2 = x.shape
+    if T2 != T or D2 != D:
+        raise ValueError("shape mismatch")
+    st, sh, sd = x.stride()
+    if T and ((sd != 1 and D > 1) or (sh != D and H > 1)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+    return H, st if T > 1 else H * D
 
 
 def _tables_lens(block_tables, context_lens, S: int, bs: int, max_context_len) -> tuple[int, int]:
     """Checks the batch metadata; (max_blocks_per_seq, max_context_len)."""
-    torch = _torch()
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+    i32 = _torch().int32
+    if block_tables.dtype != i32 or context_lens.dtype != i32:
         raise TypeError("block_tables and context_lens must be int32")
     if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
         raise ValueError("batch metadata mismatch")
     MB = block_tables.shape[1]
-    mcl = min(MB * bs, 2**31 - 1) if max_context_len is None else int(max_context_len)
-    if mcl > 2**31 - 1:
-        raise ValueError("max_context_len must be below 2^31")
-    return max(MB, 1), mcl
+    return max(MB, 1), min(MB * bs, 2**31 - 1) if max_context_len is None else int(max_context_len)
 
 
 def rope_reshape_and_cache(q, k_new, v_new, cos_sin, positions, k_cache, v_cache, slot_mapping,
@@ -741,28 +767,34 @@ def rope_reshape_and_cache(q, k_new, v_new, cos_sin, positions, k_cache, v_cache
     with ``k_scale`` and ``v_scale`` as for :func:`reshape_and_cache_fp8`. A negative
     slot stores nothing; a negative position with it leaves the row of ``q_out`` too."""
     torch = _torch()
-    dev = _cuda(k_cache, v_cache, cos_sin, positions, slot_mapping)
-    strides = [_rows(x, n, dev) for x, n in ((q, "q"), (k_new, "k_new"), (v_new, "v_new"))]
+    idx = _index(k_cache, v_cache, cos_sin, positions, slot_mapping)
+    NB, Hkv, bs, D = k_cache.shape
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("shape mismatch")
+    T, = positions.shape
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    strides.append(_rows(q_out, "q_out", dev))
+        q_out = q.new_empty(q.shape)
+    dtype = q.dtype
+    if not dtype == k_new.dtype == v_new.dtype == q_out.dtype:
+        raise TypeError("dtype mismatch")
+    Hq, q_stride = _rows(q, "q", idx, T, D)
+    Hk, k_stride = _rows(k_new, "k_new", idx, T, D)
+    Hv, v_stride = _rows(v_new, "v_new", idx, T, D)
+    Ho, o_stride = _rows(q_out, "q_out", idx, T, D)
+    if Hk != Hkv or Hv != Hkv or Ho != Hq or slot_mapping.shape != (T,):
+        raise ValueError("shape mismatch")
     if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int64:
         raise TypeError("positions and slot_mapping must be int64")
     if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
         raise TypeError("cos_sin must be float32 [max_positions, rot_dim]")
-    if not (q.dtype == k_new.dtype == v_new.dtype == q_out.dtype):
-        raise TypeError("dtype mismatch")
-    cache_code = _cache_code(k_cache, v_cache, q.dtype)
-    T, Hq, D = q.shape
-    NB, Hkv, bs, D2 = k_cache.shape
-    if (k_new.shape != (T, Hkv, D) or v_new.shape != k_new.shape or D2 != D or
-            q_out.shape != q.shape or positions.shape != (T,) or slot_mapping.shape != (T,)):
-        raise ValueError("shape mismatch")
-    ks, vs = _scale_ptrs(k_scale, v_scale, cache_code, Hkv, dev)
-    _call(dev, lib().rope_reshape_and_cache, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
-          q_out.data_ptr(), *strides, cos_sin.data_ptr(), positions.data_ptr(), cos_sin.shape[0],
-          cos_sin.shape[1], 1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(),
-          slot_mapping.data_ptr(), ks, vs, T, Hq, Hkv, D, bs, NB, _code(q), cache_code)
+    code = _cache_code(k_cache, v_cache, dtype)
+    ks, vs = _scale_ptrs(k_scale, v_scale, code, Hkv, idx)
+    far, rot = cos_sin.shape
+    _call(idx, KVP_CALL_ROPE_RESHAPE_AND_CACHE, _ROPE, q.data_ptr(), k_new.data_ptr(),
+          v_new.data_ptr(), q_out.data_ptr(), q_stride, k_stride, v_stride, o_stride,
+          cos_sin.data_ptr(), positions.data_ptr(), far, rot, 1 if interleaved else 0,
+          k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), ks, vs, T, Hq, Hkv, D,
+          bs, NB, _code(q), code)
     return q_out
 
 
@@ -777,22 +809,23 @@ def update_key_bounds(k_cache, key_bounds, block_tables, context_lens, *, new_to
     bound). The bounds have the cache's dtype, or float16 (the codes' values) over an
     E4M3 cache."""
     torch = _torch()
-    dev = _cuda(k_cache, key_bounds, block_tables, context_lens)
-    code = _cache_code(k_cache, k_cache, k_cache.dtype)
+    idx = _index(k_cache, key_bounds, block_tables, context_lens)
     NB, Hkv, bs, D = k_cache.shape
+    code = KVP_FP8_E4M3 if _is_e4m3(k_cache) else _code(k_cache)
     if key_bounds.shape != (NB, Hkv, 2, D):
         raise ValueError("key_bounds must be [NB, Hkv, 2, D]")
     if key_bounds.dtype != (torch.float16 if code == KVP_FP8_E4M3 else k_cache.dtype):
         raise TypeError("key_bounds must have the cache's dtype (float16 over an E4M3 cache)")
     S = block_tables.shape[0]
     MB, mcl = _tables_lens(block_tables, context_lens, S, bs, max_context_len)
-    new_ptr = None
+    new_ptr = 0
     if new_tokens is not None:
-        if _cuda(new_tokens) != dev or new_tokens.dtype != torch.int32 or new_tokens.shape != (S,):
+        if (_index(new_tokens) != idx or new_tokens.dtype != torch.int32 or
+                new_tokens.shape != (S,)):
             raise ValueError("new_tokens must be CUDA int32 [S] on the cache's device")
         new_ptr = new_tokens.data_ptr()
     most = mcl if max_new_tokens is None else int(max_new_tokens)
-    _call(dev, lib().update_key_bounds, k_cache.data_ptr(), key_bounds.data_ptr(),
+    _call(idx, KVP_CALL_UPDATE_KEY_BOUNDS, _BOUNDS, k_cache.data_ptr(), key_bounds.data_ptr(),
           block_tables.data_ptr(), context_lens.data_ptr(), new_ptr, S, Hkv, D, bs, NB, MB, mcl,
           most, code)
 
@@ -807,26 +840,26 @@ def select_blocks(q, key_bounds, block_tables, context_lens, out=None, *, block_
     upper bound on the group's logits from ``key_bounds`` (see :func:`update_key_bounds`);
     a context of at most ``num_selected`` blocks keeps them all."""
     torch = _torch()
-    dev = _cuda(q, key_bounds, block_tables, context_lens)
+    idx = _index(q, key_bounds, block_tables, context_lens)
     S, Hq, D = q.shape
-    if key_bounds.dim() != 4 or key_bounds.shape[2] != 2 or key_bounds.shape[3] != D:
+    NB, Hkv, two, D2 = key_bounds.shape
+    if two != 2 or D2 != D:
         raise ValueError("key_bounds must be [NB, Hkv, 2, D]")
-    NB, Hkv = key_bounds.shape[:2]
     if key_bounds.dtype == q.dtype:
         code = _code(q)
     elif key_bounds.dtype == torch.float16:
         code = KVP_FP8_E4M3
     else:
         raise TypeError("key_bounds must have q's dtype, or float16 (bounds of an E4M3 cache)")
-    MB, mcl = _tables_lens(block_tables, context_lens, S, int(block_size), max_context_len)
-    keep = int(num_selected)
+    bs, keep = int(block_size), int(num_selected)
+    MB, mcl = _tables_lens(block_tables, context_lens, S, bs, max_context_len)
     if out is None:
-        out = torch.empty((S, Hkv, max(keep, 0)), dtype=torch.int32, device=dev)
-    elif _cuda(out) != dev or out.dtype != torch.int32 or out.shape != (S, Hkv, keep):
+        out = context_lens.new_empty((S, Hkv, max(keep, 0)))
+    elif _index(out) != idx or out.dtype != torch.int32 or out.shape != (S, Hkv, keep):
         raise ValueError("out must be CUDA int32 [S, Hkv, num_selected]")
-    _call(dev, lib().select_blocks, q.data_ptr(), key_bounds.data_ptr(), block_tables.data_ptr(),
-          context_lens.data_ptr(), out.data_ptr(), S, Hq, Hkv, D, int(block_size), NB, MB, mcl,
-          keep, int(num_sink), int(num_recent), _code(q), code)
+    _call(idx, KVP_CALL_SELECT_BLOCKS, _SELECT, q.data_ptr(), key_bounds.data_ptr(),
+          block_tables.data_ptr(), context_lens.data_ptr(), out.data_ptr(), S, Hq, Hkv, D, bs, NB,
+          MB, mcl, keep, int(num_sink), int(num_recent), _code(q), code)
     return out
 
 
@@ -839,24 +872,25 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, block_tables, context_len
     The caches are of q's dtype, or E4M3 with ``k_scale`` and ``v_scale`` (CUDA float32
     ``[Hkv]``). A row whose list leaves no token is zero."""
     torch = _torch()
-    dev = _cuda(q, k_cache, v_cache, block_tables, context_lens, selected)
+    idx = _index(q, k_cache, v_cache, block_tables, context_lens, selected)
     S, Hq, D = q.shape
-    code = _cache_code(k_cache, v_cache, q.dtype)
     NB, Hkv, bs, D2 = k_cache.shape
-    if D2 != D:
+    if D2 != D or v_cache.shape != k_cache.shape:
         raise ValueError("q / cache mismatch")
-    if selected.dtype != torch.int32 or selected.dim() != 3 or selected.shape[:2] != (S, Hkv):
+    S2, Hkv2, keep = selected.shape
+    if selected.dtype != torch.int32 or S2 != S or Hkv2 != Hkv:
         raise ValueError("selected must be int32 [S, Hkv, n]")
+    code = _cache_code(k_cache, v_cache, q.dtype)
     MB, mcl = _tables_lens(block_tables, context_lens, S, bs, max_context_len)
-    ks, vs = _scale_ptrs(k_scale, v_scale, code, Hkv, dev)
+    ks, vs = _scale_ptrs(k_scale, v_scale, code, Hkv, idx)
     if out is None:
         out = torch.empty_like(q)
-    elif _cuda(out) != dev or out.shape != q.shape or out.dtype != q.dtype:
+    elif _index(out) != idx or out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out mismatch")
-    _call(dev, lib().paged_attention_decode_sparse, q.data_ptr(), k_cache.data_ptr(),
+    _call(idx, KVP_CALL_DECODE_SPARSE, _SPARSE, q.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), ks, vs, block_tables.data_ptr(), context_lens.data_ptr(),
-          selected.data_ptr(), S, Hq, Hkv, D, bs, NB, MB, mcl, selected.shape[2], float(scale),
-          out.data_ptr(), _code(q), code)
+          selected.data_ptr(), S, Hq, Hkv, D, bs, NB, MB, mcl, keep, float(scale), out.data_ptr(),
+          _code(q), code)
     return out
 
 

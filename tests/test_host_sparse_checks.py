@@ -2,6 +2,7 @@
 KVP_ERR_INVALID before any CUDA call. The pointers are fake and never dereferenced."""
 
 import ctypes as C
+import struct
 
 import pytest
 
@@ -33,9 +34,21 @@ DECODE = dict(q=p(1), k=p(2), v=p(3), kscale=None, vscale=None, t=p(4), l=p(5), 
               st=None)
 
 
+def words(args):
+    """The arguments as 64-bit words: pointers and integers, floats as doubles."""
+    vals = [(a.value or 0) if isinstance(a, C.c_void_p) else 0 if a is None else a for a in args]
+    return struct.pack("".join("d" if isinstance(v, float) else "q" for v in vals), *vals)
+
+
 def call(fn, base, **kw):
+    """The entry point's status, the same for the plain and the one-block call."""
     assert set(kw) <= set(base)
-    return fn(*{**base, **kw}.values())
+    args = list({**base, **kw}.values())
+    rc = fn(*args)
+    code = ("rope_reshape_and_cache", "update_key_bounds", "select_blocks",
+            "paged_attention_decode_sparse").index(fn.__name__)
+    assert _lib.lib().kvp_call_words(code, words(args), len(args)) == rc
+    return rc
 
 
 @pytest.mark.parametrize("bad", [
@@ -88,3 +101,15 @@ def test_empty_calls_are_no_ops(lib):
     assert call(lib.update_key_bounds, BOUNDS, mnew=0) == OK
     assert call(lib.select_blocks, SELECT, S=0, q=None, out=None) == OK
     assert call(lib.paged_attention_decode_sparse, DECODE, S=0, q=None, out=None) == OK
+
+
+def test_one_block_call_refuses(lib):
+    args = list(DECODE.values())
+    for code, w, n in ((-1, words(args), 22), (4, words(args), 22), (3, None, 22),
+                       (3, words(args), 21), (2, words(args), 22)):
+        assert lib.kvp_call_words(code, w, n) == INVALID
+    for base, code, key in ((ROPE, 0, "T"), (ROPE, 0, "rot"), (BOUNDS, 1, "mcl"),
+                            (SELECT, 2, "keep"), (DECODE, 3, "cdt")):
+        args = list({**base, key: 2**32 + base[key]}.values())
+        assert lib.kvp_call_words(code, words(args), len(args)) == INVALID
+        assert b"out of range" in lib.kvp_last_error_message()
