@@ -674,7 +674,8 @@ def attention_decode_vcache(q, vc: VCache, seq_slots, context_lens, scale: float
 
 # The calls below take their arguments in one block (``kvp_call_words``): per argument
 # that is a fraction of what ctypes takes, and these calls run once per layer and step.
-_ROPE, _BOUNDS, _SELECT, _SPARSE = (struct.Struct(f) for f in ("27q", "15q", "19q", "17qd4q"))
+_ROPE, _BOUNDS, _SELECT, _SPARSE, _WORD = (struct.Struct(f) for f in
+                                           ("26q", "14q", "18q", "17qd3q", "q"))
 
 
 def _index(*ts) -> int:
@@ -688,29 +689,42 @@ def _index(*ts) -> int:
     return idx
 
 
-def _call(idx: int, call: int, words: struct.Struct, *args) -> None:
-    """Entry point ``call`` with ``args`` and the current stream of device ``idx``, with
-    that device current."""
+def _call(idx: int, call: int, words: bytes, num_words: int) -> None:
+    """Entry point ``call`` with ``words`` and, as the last one, the current stream of
+    device ``idx``, with that device current."""
     torch = _torch()
     if torch.cuda.current_device() == idx:
-        stream = torch._C._cuda_getCurrentRawStream(idx)
-        check(lib().kvp_call_words(call, words.pack(*args, stream), len(args) + 1))
+        words += _WORD.pack(torch._C._cuda_getCurrentRawStream(idx))
+        rc = lib().kvp_call_words(call, words, num_words)
     else:
         with torch.cuda.device(idx):
-            stream = torch._C._cuda_getCurrentRawStream(idx)
-            check(lib().kvp_call_words(call, words.pack(*args, stream), len(args) + 1))
+            words += _WORD.pack(torch._C._cuda_getCurrentRawStream(idx))
+            rc = lib().kvp_call_words(call, words, num_words)
+    if rc:
+        check(rc)
 
 
-def _cache_code(k_cache, v_cache, dtype) -> int:
-    """Cache type of pools beside 16-bit rows of ``dtype``: theirs, or E4M3."""
-    kt = k_cache.dtype
-    if kt != v_cache.dtype:
-        raise TypeError("the caches must share a dtype")
-    if kt == dtype:
-        return _code(k_cache)
-    if not _is_e4m3(k_cache):
+_codes_of = {}  # torch dtype -> element type of a pool
+
+
+def _codes() -> dict:
+    if not _codes_of:
+        torch = _torch()
+        _codes_of.update({torch.float16: KVP_F16, torch.bfloat16: KVP_BF16,
+                          torch.uint8: KVP_FP8_E4M3, torch.float8_e4m3fn: KVP_FP8_E4M3})
+    return _codes_of
+
+
+def _types(rows, k_cache, v_cache) -> tuple[int, int]:
+    """Element types of 16-bit rows and of pools beside them: the same, or E4M3."""
+    codes = _codes()
+    dtype, kt = rows.dtype, k_cache.dtype
+    code, cache = codes.get(dtype), codes.get(kt)
+    if v_cache.dtype != kt or code is None or code == KVP_FP8_E4M3:
+        raise TypeError("16-bit rows and caches of one dtype are needed")
+    if cache != code and cache != KVP_FP8_E4M3:
         raise TypeError("the caches must have the dtype of the rows, or be E4M3")
-    return KVP_FP8_E4M3
+    return code, cache
 
 
 def _scale_ptrs(k_scale, v_scale, cache_code, Hkv, idx):
@@ -728,20 +742,19 @@ def _scale_ptrs(k_scale, v_scale, cache_code, Hkv, idx):
     return k_scale.data_ptr(), v_scale.data_ptr()
 
 
-def _rows(x, name: str, idx: int, T: int, D: int) -> tuple[int, int]:
-    """Checks ``x [T, heads, D]`` on device ``idx``, each token's heads contiguous;
-    (heads, elements between tokens)."""
+def _rows(x, idx: int, T: int, H: int, D: int, dtype) -> int:
+    """Checks ``x [T, H, D]`` of ``dtype`` on device ``idx``, each token's heads
+    contiguous; the elements between two tokens."""
     if x.get_device() != idx:
         raise ValueError("all tensors must be on the same CUDA device")
-    if x.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    T2, H, D2 = x.shape
-    if T2 != T or D2 != D:
+    if x.dtype != dtype:
+        raise TypeError("dtype mismatch")
+    if x.shape != (T, H, D):
         raise ValueError("shape mismatch")
     st, sh, sd = x.stride()
     if T and ((sd != 1 and D > 1) or (sh != D and H > 1)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return H, st if T > 1 else H * D
+        raise ValueError("the heads of a token must be contiguous")
+    return st if T > 1 else H * D
 
 
 def _tables_lens(block_tables, context_lens, S: int, bs: int, max_context_len) -> tuple[int, int]:
@@ -749,10 +762,11 @@ def _tables_lens(block_tables, context_lens, S: int, bs: int, max_context_len) -
     i32 = _torch().int32
     if block_tables.dtype != i32 or context_lens.dtype != i32:
         raise TypeError("block_tables and context_lens must be int32")
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+    S2, MB = block_tables.shape
+    L, = context_lens.shape
+    if S2 != S or L != S:
         raise ValueError("batch metadata mismatch")
-    MB = block_tables.shape[1]
-    return max(MB, 1), min(MB * bs, 2**31 - 1) if max_context_len is None else int(max_context_len)
+    return MB or 1, min(MB * bs, 2**31 - 1) if max_context_len is None else int(max_context_len)
 
 
 def rope_reshape_and_cache(q, k_new, v_new, cos_sin, positions, k_cache, v_cache, slot_mapping,
@@ -768,33 +782,32 @@ def rope_reshape_and_cache(q, k_new, v_new, cos_sin, positions, k_cache, v_cache
     slot stores nothing; a negative position with it leaves the row of ``q_out`` too."""
     torch = _torch()
     idx = _index(k_cache, v_cache, cos_sin, positions, slot_mapping)
-    NB, Hkv, bs, D = k_cache.shape
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("shape mismatch")
-    T, = positions.shape
-    if q_out is None:
-        q_out = q.new_empty(q.shape)
-    dtype = q.dtype
-    if not dtype == k_new.dtype == v_new.dtype == q_out.dtype:
-        raise TypeError("dtype mismatch")
-    Hq, q_stride = _rows(q, "q", idx, T, D)
-    Hk, k_stride = _rows(k_new, "k_new", idx, T, D)
-    Hv, v_stride = _rows(v_new, "v_new", idx, T, D)
-    Ho, o_stride = _rows(q_out, "q_out", idx, T, D)
-    if Hk != Hkv or Hv != Hkv or Ho != Hq or slot_mapping.shape != (T,):
+    code, cache_code = _types(q, k_cache, v_cache)
+    dtype, pool = q.dtype, k_cache.shape
+    NB, Hkv, bs, D = pool
+    T, Hq, _ = q.shape
+    far, rot = cos_sin.shape
+    T2, = positions.shape
+    T3, = slot_mapping.shape
+    if v_cache.shape != pool or T2 != T or T3 != T:
         raise ValueError("shape mismatch")
     if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int64:
         raise TypeError("positions and slot_mapping must be int64")
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+    if cos_sin.dtype != torch.float32:
         raise TypeError("cos_sin must be float32 [max_positions, rot_dim]")
-    code = _cache_code(k_cache, v_cache, dtype)
-    ks, vs = _scale_ptrs(k_scale, v_scale, code, Hkv, idx)
-    far, rot = cos_sin.shape
-    _call(idx, KVP_CALL_ROPE_RESHAPE_AND_CACHE, _ROPE, q.data_ptr(), k_new.data_ptr(),
-          v_new.data_ptr(), q_out.data_ptr(), q_stride, k_stride, v_stride, o_stride,
-          cos_sin.data_ptr(), positions.data_ptr(), far, rot, 1 if interleaved else 0,
-          k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), ks, vs, T, Hq, Hkv, D,
-          bs, NB, _code(q), code)
+    q_stride = _rows(q, idx, T, Hq, D, dtype)
+    k_stride = _rows(k_new, idx, T, Hkv, D, dtype)
+    v_stride = _rows(v_new, idx, T, Hkv, D, dtype)
+    if q_out is None:
+        q_out, o_stride = q.new_empty((T, Hq, D)), Hq * D
+    else:
+        o_stride = _rows(q_out, idx, T, Hq, D, dtype)
+    ks, vs = _scale_ptrs(k_scale, v_scale, cache_code, Hkv, idx)
+    _call(idx, KVP_CALL_ROPE_RESHAPE_AND_CACHE,
+          _ROPE.pack(q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), q_out.data_ptr(), q_stride,
+                     k_stride, v_stride, o_stride, cos_sin.data_ptr(), positions.data_ptr(), far,
+                     rot, 1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(),
+                     slot_mapping.data_ptr(), ks, vs, T, Hq, Hkv, D, bs, NB, code, cache_code), 27)
     return q_out
 
 
@@ -811,23 +824,25 @@ def update_key_bounds(k_cache, key_bounds, block_tables, context_lens, *, new_to
     torch = _torch()
     idx = _index(k_cache, key_bounds, block_tables, context_lens)
     NB, Hkv, bs, D = k_cache.shape
-    code = KVP_FP8_E4M3 if _is_e4m3(k_cache) else _code(k_cache)
+    code = _codes().get(k_cache.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {k_cache.dtype}")
     if key_bounds.shape != (NB, Hkv, 2, D):
         raise ValueError("key_bounds must be [NB, Hkv, 2, D]")
     if key_bounds.dtype != (torch.float16 if code == KVP_FP8_E4M3 else k_cache.dtype):
         raise TypeError("key_bounds must have the cache's dtype (float16 over an E4M3 cache)")
-    S = block_tables.shape[0]
+    S, _ = block_tables.shape
     MB, mcl = _tables_lens(block_tables, context_lens, S, bs, max_context_len)
     new_ptr = 0
     if new_tokens is not None:
-        if (_index(new_tokens) != idx or new_tokens.dtype != torch.int32 or
-                new_tokens.shape != (S,)):
+        if (new_tokens.dtype != torch.int32 or new_tokens.shape != (S,) or
+                _index(new_tokens) != idx):
             raise ValueError("new_tokens must be CUDA int32 [S] on the cache's device")
         new_ptr = new_tokens.data_ptr()
     most = mcl if max_new_tokens is None else int(max_new_tokens)
-    _call(idx, KVP_CALL_UPDATE_KEY_BOUNDS, _BOUNDS, k_cache.data_ptr(), key_bounds.data_ptr(),
-          block_tables.data_ptr(), context_lens.data_ptr(), new_ptr, S, Hkv, D, bs, NB, MB, mcl,
-          most, code)
+    _call(idx, KVP_CALL_UPDATE_KEY_BOUNDS,
+          _BOUNDS.pack(k_cache.data_ptr(), key_bounds.data_ptr(), block_tables.data_ptr(),
+                       context_lens.data_ptr(), new_ptr, S, Hkv, D, bs, NB, MB, mcl, most, code), 15)
 
 
 def select_blocks(q, key_bounds, block_tables, context_lens, out=None, *, block_size: int,
@@ -845,21 +860,23 @@ def select_blocks(q, key_bounds, block_tables, context_lens, out=None, *, block_
     NB, Hkv, two, D2 = key_bounds.shape
     if two != 2 or D2 != D:
         raise ValueError("key_bounds must be [NB, Hkv, 2, D]")
-    if key_bounds.dtype == q.dtype:
-        code = _code(q)
-    elif key_bounds.dtype == torch.float16:
-        code = KVP_FP8_E4M3
-    else:
-        raise TypeError("key_bounds must have q's dtype, or float16 (bounds of an E4M3 cache)")
+    code, cache_code = _codes().get(q.dtype), _codes().get(key_bounds.dtype)
+    if code is None or code == KVP_FP8_E4M3 or cache_code is None:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    if cache_code != code:
+        if cache_code != KVP_F16:
+            raise TypeError("key_bounds must have q's dtype, or float16 (bounds of an E4M3 cache)")
+        cache_code = KVP_FP8_E4M3
     bs, keep = int(block_size), int(num_selected)
     MB, mcl = _tables_lens(block_tables, context_lens, S, bs, max_context_len)
     if out is None:
         out = context_lens.new_empty((S, Hkv, max(keep, 0)))
     elif _index(out) != idx or out.dtype != torch.int32 or out.shape != (S, Hkv, keep):
         raise ValueError("out must be CUDA int32 [S, Hkv, num_selected]")
-    _call(idx, KVP_CALL_SELECT_BLOCKS, _SELECT, q.data_ptr(), key_bounds.data_ptr(),
-          block_tables.data_ptr(), context_lens.data_ptr(), out.data_ptr(), S, Hq, Hkv, D, bs, NB,
-          MB, mcl, keep, int(num_sink), int(num_recent), _code(q), code)
+    _call(idx, KVP_CALL_SELECT_BLOCKS,
+          _SELECT.pack(q.data_ptr(), key_bounds.data_ptr(), block_tables.data_ptr(),
+                       context_lens.data_ptr(), out.data_ptr(), S, Hq, Hkv, D, bs, NB, MB, mcl, keep,
+                       int(num_sink), int(num_recent), code, cache_code), 19)
     return out
 
 
@@ -873,24 +890,26 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, block_tables, context_len
     ``[Hkv]``). A row whose list leaves no token is zero."""
     torch = _torch()
     idx = _index(q, k_cache, v_cache, block_tables, context_lens, selected)
+    code, cache_code = _types(q, k_cache, v_cache)
     S, Hq, D = q.shape
-    NB, Hkv, bs, D2 = k_cache.shape
-    if D2 != D or v_cache.shape != k_cache.shape:
-        raise ValueError("q / cache mismatch")
+    pool = k_cache.shape
+    NB, Hkv, bs, D2 = pool
     S2, Hkv2, keep = selected.shape
+    if D2 != D or v_cache.shape != pool:
+        raise ValueError("q / cache mismatch")
     if selected.dtype != torch.int32 or S2 != S or Hkv2 != Hkv:
         raise ValueError("selected must be int32 [S, Hkv, n]")
-    code = _cache_code(k_cache, v_cache, q.dtype)
     MB, mcl = _tables_lens(block_tables, context_lens, S, bs, max_context_len)
-    ks, vs = _scale_ptrs(k_scale, v_scale, code, Hkv, idx)
+    ks, vs = _scale_ptrs(k_scale, v_scale, cache_code, Hkv, idx)
     if out is None:
         out = torch.empty_like(q)
-    elif _index(out) != idx or out.shape != q.shape or out.dtype != q.dtype:
+    elif out.dtype != q.dtype or out.shape != q.shape or _index(out) != idx:
         raise ValueError("out mismatch")
-    _call(idx, KVP_CALL_DECODE_SPARSE, _SPARSE, q.data_ptr(), k_cache.data_ptr(),
-          v_cache.data_ptr(), ks, vs, block_tables.data_ptr(), context_lens.data_ptr(),
-          selected.data_ptr(), S, Hq, Hkv, D, bs, NB, MB, mcl, keep, float(scale), out.data_ptr(),
-          _code(q), code)
+    _call(idx, KVP_CALL_DECODE_SPARSE,
+          _SPARSE.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs,
+                       block_tables.data_ptr(), context_lens.data_ptr(), selected.data_ptr(), S, Hq,
+                       Hkv, D, bs, NB, MB, mcl, keep, float(scale), out.data_ptr(), code,
+                       cache_code), 22)
     return out
 
 

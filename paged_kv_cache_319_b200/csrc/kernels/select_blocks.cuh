@@ -6,23 +6,38 @@
 //   Q+ = sum_g max(q[g], 0),  Q- = sum_g min(q[g], 0),
 // which is sum_g sum_d max(q[g][d] M[d], q[g][d] m[d]) and so no smaller than
 // the sum over the group of any of the block's logits. A score costs 2 D
-// multiply-adds whatever the group's size. Sums are fp64: 16-bit products are exact there and
-// so, for all practical data, are the sums, which makes the choice independent
-// of the summation order.
+// multiply-adds whatever the group's size. The order is that of fp64 sums:
+// 16-bit products are exact there and so, for all practical data, are the sums,
+// which makes the choice independent of the summation order.
 //
-// One cluster of up to 8 CTAs serves a (sequence, KV head). Each CTA scores a
-// contiguous range of blocks (a warp reads a block's 4 D bytes of bounds at 16
-// bytes per lane) and keeps the scores as order-preserving 64-bit keys in
-// shared memory. The threshold is found by zooming: a 1024-bin histogram of
-// the active key range, merged over the cluster through distributed shared
-// memory, names the bin that holds the last kept key; that bin is the next
-// range. Then the CTAs write their kept blocks in ascending order at offsets
-// from a prefix sum over warps and CTAs.
+// Bound by HBM (the context's bounds are read once) if the scores cost little:
+// in fp64 a block's 2 D conversions and multiply-adds and the reduction over the
+// lanes took 4.4 times as long as its bytes. So the scores are first taken on the
+// tensor cores in fp32, 16 blocks (A rows) against the weights split into three
+// 16-bit parts (columns 0 to 2 of B), with a bound E on their error; only blocks
+// whose fp32 score lies within 2 E of the cut, usually a handful, are scored
+// in fp64. Where many lie there (equal blocks, a zero query) or E is not finite,
+// every block is.
+//
+// E: the weights are scaled by a power of two to at most 2^15, so three parts
+// leave 2^-24 of a weight or less; the MMAs' fp32 sums of 2 D products in steps
+// of 16 are off by at most 2^-16 of the sum of the products' sizes even if each
+// addend is cut to 24 bits; S = max |bound| * sum |weight| is no less than that
+// sum, and E = 2^-15 S + 2^-117 (products below fp32's normal range) covers it
+// twice.
+//
+// One cluster of up to 8 CTAs serves a (sequence, KV head); each CTA scores a
+// contiguous range of blocks and keeps the scores as order-preserving keys in
+// shared memory. The cut is found by zooming: a 1024-bin histogram of the active
+// key range, merged over the cluster through distributed shared memory, names
+// the bin that holds the last kept key. The kept blocks are written in ascending
+// order at offsets from a prefix sum over warps and CTAs.
 #pragma once
 
 #include <cooperative_groups.h>
 
 #include "common.cuh"
+#include "mma_sync.cuh"
 
 namespace kvp {
 namespace dev {
@@ -39,32 +54,139 @@ struct SelectArgs {
   int32_t keep, sink, recent;
 };
 
-constexpr int kSelWarps = 16;
+constexpr int kSelWarps = 8;
 constexpr int kSelThreads = kSelWarps * 32;
 constexpr int kSelBins = 1024;
 constexpr int kSelLog2Bins = 10;
+constexpr int kSelNear = 64;  // most blocks near the cut that are scored again
 
-// Order-preserving map of fp64 to uint64; NaN above everything, -0 equal to 0.
+// Order-preserving maps to unsigned integers. fp64: NaN above everything, -0 equal
+// to 0. 0 is below the key of every number.
 __device__ __forceinline__ uint64_t score_key(double x) {
   if (x != x) return ~0ull;
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
   return (u >> 63) ? ~u : (u | (1ull << 63));
 }
+__device__ __forceinline__ uint32_t approx_key(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float approx_value(uint32_t k) {
+  return __uint_as_float((k >> 31) ? (k ^ 0x80000000u) : ~k);
+}
+
+// The cluster's shared state of one selection.
+struct SelectShared {
+  uint32_t hist[2][kSelBins];
+  uint64_t range_lo[kSelWarps], range_hi[kSelWarps];
+  uint64_t cta_lo, cta_hi;       // range of the CTA's keys
+  uint32_t warp_max[kSelWarps], cta_max;  // largest |bound|, 16-bit pattern
+  uint32_t warp_sum[kSelWarps];
+  uint32_t found[3];             // bin, keys above it, keys in it
+  uint32_t take[2][kSelWarps + 1];  // kept / tied keys per warp, and of the CTA
+  uint32_t above, near;          // this CTA's keys past the near ones, near ones
+  uint32_t near_at[kSelNear];    // their places, and fp64 keys
+  uint64_t near_key[kSelNear];
+  uint32_t all_at[kSelNear];     // the cluster's, gathered
+  uint64_t all_key[kSelNear];
+  uint32_t near_kept[8];         // kept near keys of each rank
+};
+
+// One zoom: the bin of keys[0, count) within [lo, hi] (over the cluster) that
+// holds the need-th largest, in found; hist[phase] is used, hist[phase ^ 1] is
+// cleared for the next. `found` is written again only after the next cluster.sync.
+template <typename Key, typename Cluster>
+__device__ __forceinline__ int zoom(SelectShared& sh, Cluster& cluster, const Key* keys, int count,
+                                    Key lo, Key hi, uint32_t need, int phase) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t nranks = cluster.num_blocks();
+  const int bits = 64 - __clzll(static_cast<long long>(hi - lo));
+  const int shift = bits > kSelLog2Bins ? bits - kSelLog2Bins : 0;
+  uint32_t* mine = sh.hist[phase];
+  for (int i = tid; i < count; i += kSelThreads) {
+    const Key k = keys[i];
+    if (k >= lo && k <= hi) atomicAdd(&mine[uint32_t((k - lo) >> shift)], 1u);
+  }
+  cluster.sync();
+  // each thread: neighbouring bins of the merged histogram, highest first
+  constexpr int PER = kSelBins / kSelThreads;
+  uint32_t bin[PER], total = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) bin[j] = 0;
+  for (uint32_t r = 0; r < nranks; ++r) {
+    const uint32_t* theirs = cluster.map_shared_rank(mine, r);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) bin[j] += theirs[kSelBins - 1 - (tid * PER + j)];
+  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j) total += bin[j];
+  uint32_t incl = total;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, m);
+    if (lane >= m) incl += v;
+  }
+  if (lane == 31) sh.warp_sum[warp] = incl;
+  // the other buffer was last read before this call's cluster.sync
+  for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[phase ^ 1][i] = 0;
+  __syncthreads();
+  uint32_t above = incl - total;
+  for (int i = 0; i < warp; ++i) above += sh.warp_sum[i];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    if (above < need && above + bin[j] >= need)
+      sh.found[0] = kSelBins - 1 - (tid * PER + j), sh.found[1] = above, sh.found[2] = bin[j];
+    above += bin[j];
+  }
+  __syncthreads();
+  return shift;
+}
+
+// The fp64 keys of blocks table[at[0..U)] (by a warp; every lane has them). at < 0:
+// no block, key 0 like a block id outside the pool.
+template <typename TB, int D, int U>
+__device__ __forceinline__ void exact_keys(const SelectArgs& a, const double* weight,
+                                           const int32_t* table, const int (&at)[U], uint32_t g,
+                                           uint64_t (&key)[U]) {
+  constexpr int W = D / 32;  // 2-element words per lane
+  const int lane = threadIdx.x & 31;
+  int32_t b[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) b[u] = at[u] >= 0 ? __ldg(table + at[u]) : -1;
+  uint32_t x[U][W];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (b[u] >= a.num_blocks) b[u] = -1;
+    const uint32_t* src = static_cast<const uint32_t*>(a.bounds) +
+                          (int64_t(b[u]) * a.num_kv_heads + g) * D + lane;
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[u][i] = b[u] >= 0 ? __ldg(src + i * 32) : 0u;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float2 f = Elem<TB>::to_float2(x[u][i]);
+      const double2 w = *reinterpret_cast<const double2*>(weight + (i * 32 + lane) * 2);
+      sum = fma(w.x, double(f.x), sum);
+      sum = fma(w.y, double(f.y), sum);
+    }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    key[u] = b[u] >= 0 ? score_key(sum) : 0ull;
+  }
+}
 
 // TQ: the queries' type, TB: the bounds' type.
 template <typename TQ, typename TB, int D>
-__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const SelectArgs a) {
   namespace cg = cooperative_groups;
-  constexpr int LPB = D / 4;      // lanes per block: 2 D elements, 8 per lane
-  constexpr int BPL = 32 / LPB;   // blocks per warp load
-  constexpr int U = 8 / BPL;      // loads in flight: 8 blocks per warp step
   extern __shared__ uint64_t keys[];
-  __shared__ uint32_t hist[2][kSelBins];
-  __shared__ uint64_t range_lo[kSelWarps], range_hi[kSelWarps];
-  __shared__ uint64_t cta_lo, cta_hi;
-  __shared__ uint32_t warp_sum[kSelWarps];
-  __shared__ uint32_t found[3];  // bin, keys above it, keys in it
-  __shared__ uint32_t take[2][kSelWarps + 1];  // kept / tied keys per warp, and of the CTA
+  uint32_t* keys32 = reinterpret_cast<uint32_t*>(keys);
+  __shared__ SelectShared sh;
+  __shared__ __align__(16) double weight[2 * D];    // Q+, then Q-
+  __shared__ __align__(16) uint16_t part[3][2 * D]; // their scaled 16-bit parts
 
   cg::cluster_group cluster = cg::this_cluster();
   const uint32_t nranks = cluster.num_blocks(), rank = cluster.block_rank();
@@ -77,7 +199,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     if (g == 0 && rank == 0 && tid == 0) record_error(KVP_DEVERR_CTX, s);
     ctx = ctx < 0 ? 0 : a.max_context_len;
   }
-  const int n = (ctx + (1 << a.log2_bs) - 1) >> a.log2_bs;
+  const int n = int((ctx + (int64_t(1) << a.log2_bs) - 1) >> a.log2_bs);
   int32_t* out = a.out + int64_t(unit) * a.keep;
   if (n <= a.keep) {  // every block is kept (uniform over the cluster)
     if (rank == 0)
@@ -94,181 +216,340 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
   if (need == 0) return;
   const int per = (cand + nranks - 1) / nranks;
   const int first = min(cand, int(rank) * per), count = min(cand, first + per) - first;
-
-  // ---- scores -----------------------------------------------------------------
-  const int G = a.num_q_heads / a.num_kv_heads;
-  const int sub = lane % LPB;           // lane within its block
-  const bool low = sub >= LPB / 2;      // the smallest keys' half
-  double w[8];
-  {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = 0.0;
-    const uint4* q = static_cast<const uint4*>(a.q) +
-                     (int64_t(s) * a.num_q_heads + int64_t(g) * G) * (D / 8) + sub % (LPB / 2);
-    for (int h = 0; h < G; ++h) {
-      const uint4 x = __ldg(q + h * (D / 8));
-      const uint32_t p[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = Elem<TQ>::to_float2(p[e]);
-        // comparisons that keep a NaN query
-        w[2 * e] += double(low ? (f.x > 0.f ? 0.f : f.x) : (f.x < 0.f ? 0.f : f.x));
-        w[2 * e + 1] += double(low ? (f.y > 0.f ? 0.f : f.y) : (f.y < 0.f ? 0.f : f.y));
-      }
-    }
-  }
   const int32_t* table = a.block_tables + int64_t(s) * a.max_blocks_per_seq + a.sink + first;
-  uint64_t my_lo = ~0ull, my_hi = 0;
-  for (int c0 = warp * 8; c0 < count; c0 += kSelWarps * 8) {
-    int32_t id = -1;
-    if (lane < 8 && c0 + lane < count) {
-      id = __ldg(table + c0 + lane);
-      if (id < 0 || id >= a.num_blocks) {
-        if (g == 0)
-          record_error(KVP_DEVERR_BLOCK_ID,
-                       (uint64_t(s) << 32) | uint32_t(a.sink + first + c0 + lane));
-        id = -1;
-      }
+
+  // ---- weights: fp64 sums, and their three 16-bit parts ----
+  const int G = a.num_q_heads / a.num_kv_heads;
+  float wmax = 0.f, wsum = 0.f;
+  for (int e = tid; e < 2 * D; e += kSelThreads) {
+    const bool low = e >= D;
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) +
+                        (int64_t(s) * a.num_q_heads + int64_t(g) * G) * D + (low ? e - D : e);
+    double w = 0.0;
+    for (int h = 0; h < G; ++h) {
+      const float f = Elem<TQ>::to_float2(__ldg(q + int64_t(h) * D)).x;
+      // comparisons that keep a NaN query
+      w += double(low ? (f > 0.f ? 0.f : f) : (f < 0.f ? 0.f : f));
     }
-    uint4 x[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int32_t b = __shfl_sync(0xffffffffu, id, u * BPL + lane / LPB);
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (b >= 0)
-        x[u] = __ldg(static_cast<const uint4*>(a.bounds) +
-                     (int64_t(b) * a.num_kv_heads + g) * LPB + sub);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t p[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      double sum = 0.0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = Elem<TB>::to_float2(p[e]);
-        sum = fma(w[2 * e], double(f.x), sum);
-        sum = fma(w[2 * e + 1], double(f.y), sum);
-      }
-#pragma unroll
-      for (int m = 1; m < LPB; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-      const int c = c0 + u * BPL + lane / LPB;
-      const int32_t b = __shfl_sync(0xffffffffu, id, u * BPL + lane / LPB);
-      if (sub == 0 && c < count) {
-        const uint64_t key = b >= 0 ? score_key(sum) : 0ull;
-        keys[c] = key;
-        my_lo = min(my_lo, key);
-        my_hi = max(my_hi, key);
-      }
-    }
+    weight[e] = w;
+    wmax = fmaxf(wmax, fabsf(float(w)));
   }
+  for (int m = 1; m < 32; m <<= 1) wmax = fmaxf(wmax, __shfl_xor_sync(0xffffffffu, wmax, m));
+  if (lane == 0) sh.warp_sum[warp] = __float_as_uint(wmax);
+  for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[0][i] = 0;
+  __syncthreads();
+  for (int i = 0; i < kSelWarps; ++i) wmax = fmaxf(wmax, __uint_as_float(sh.warp_sum[i]));
+  const int wexp = int(__float_as_uint(wmax) >> 23) - 127;
+  const double up = wmax > 0.f ? __hiloint2double((1023 + 14 - wexp) << 20, 0) : 1.0;
+  for (int e = tid; e < 2 * D; e += kSelThreads) {
+    double w = weight[e] * up;
 #pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    my_lo = min(my_lo, __shfl_xor_sync(0xffffffffu, my_lo, m));
-    my_hi = max(my_hi, __shfl_xor_sync(0xffffffffu, my_hi, m));
+    for (int i = 0; i < 3; ++i) {
+      const uint32_t x = Elem<TB>::from_float(float(w));
+      part[i][e] = uint16_t(x);
+      w -= double(Elem<TB>::to_float2(x).x);
+    }
+    wsum += float(fabs(weight[e] * up));
   }
-  if (lane == 0) range_lo[warp] = my_lo, range_hi[warp] = my_hi;
-  for (int i = tid; i < kSelBins; i += kSelThreads) hist[0][i] = 0;
+  for (int m = 1; m < 32; m <<= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, m);
+  __syncthreads();
+  if (lane == 0) sh.warp_sum[warp] = __float_as_uint(wsum);
+  __syncthreads();
+  wsum = 0.f;
+  for (int i = 0; i < kSelWarps; ++i) wsum += __uint_as_float(sh.warp_sum[i]);
+
+  // ---- fp32 scores: 16 blocks per warp and step ----
+  // Lane l holds rows r = l/4 and r + 8 of A and column r of B; of a row it reads
+  // 16 bytes at a time, whose words are the k positions of two MMA steps.
+  {
+    constexpr int ROW = 2 * D * 2;  // bytes of a block's bounds of one head
+    constexpr int L = ROW / 64;     // 16-byte loads per row and lane
+    const int r = lane >> 2, p = lane & 3;
+    uint4 w[L];
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      w[j] = make_uint4(0, 0, 0, 0);
+      if (r < 3) w[j] = *reinterpret_cast<const uint4*>(&part[r][j * 32 + p * 8]);
+    }
+    uint32_t big = 0, my_lo = ~0u, my_hi = 0;
+    auto locate = [&](int c0) {
+      int32_t id = -1;
+      const int c = c0 + (lane & 15);
+      if (c < count) {
+        id = __ldg(table + c);
+        if (id < 0 || id >= a.num_blocks) {
+          if (g == 0 && lane < 16)
+            record_error(KVP_DEVERR_BLOCK_ID, (uint64_t(s) << 32) | uint32_t(a.sink + first + c));
+          id = -1;
+        }
+      }
+      return id;
+    };
+    int32_t id = locate(warp * 16);
+    for (int c0 = warp * 16; c0 < count; c0 += kSelWarps * 16) {
+      const int32_t b0 = __shfl_sync(0xffffffffu, id, r), b1 = __shfl_sync(0xffffffffu, id, r + 8);
+      uint4 x[2][L];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int32_t b = y ? b1 : b0;
+        const char* src = static_cast<const char*>(a.bounds) +
+                          (int64_t(b) * a.num_kv_heads + g) * ROW + p * 16;
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+          x[y][j] = make_uint4(0, 0, 0, 0);
+          if (b >= 0) x[y][j] = ld_stream(src + j * 64);
+        }
+      }
+      id = locate(c0 + kSelWarps * 16);
+      float z[2][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[0][e] = z[1][e] = 0.f;
+#pragma unroll
+      for (int j = 0; j < L; ++j) {
+        const uint32_t a0[4] = {x[0][j].x, x[1][j].x, x[0][j].y, x[1][j].y};
+        const uint32_t a1[4] = {x[0][j].z, x[1][j].z, x[0][j].w, x[1][j].w};
+        mma16816<TB>(z[0], a0, w[j].x, w[j].y);
+        mma16816<TB>(z[1], a1, w[j].z, w[j].w);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          big = __vmaxu2(big, x[y][j].x & 0x7fff7fffu);
+          big = __vmaxu2(big, x[y][j].y & 0x7fff7fffu);
+          big = __vmaxu2(big, x[y][j].z & 0x7fff7fffu);
+          big = __vmaxu2(big, x[y][j].w & 0x7fff7fffu);
+        }
+      }
+      // columns 0 and 1 are in the lanes of p = 0, column 2 in those of p = 1
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const float c01 = (z[0][2 * y] + z[1][2 * y]) + (z[0][2 * y + 1] + z[1][2 * y + 1]);
+        const float c2 = __shfl_down_sync(0xffffffffu, z[0][2 * y] + z[1][2 * y], 1);
+        const int c = c0 + y * 8 + r;
+        if (p == 0 && c < count) {
+          const uint32_t k = (y ? b1 : b0) >= 0 ? approx_key(c01 + c2) : 0u;
+          keys32[c] = k;
+          my_lo = min(my_lo, k);
+          my_hi = max(my_hi, k);
+        }
+      }
+    }
+    big = max(big >> 16, big & 0xffffu);
+    big = __reduce_max_sync(0xffffffffu, big);
+    my_lo = __reduce_min_sync(0xffffffffu, my_lo);
+    my_hi = __reduce_max_sync(0xffffffffu, my_hi);
+    if (lane == 0) sh.range_lo[warp] = my_lo, sh.range_hi[warp] = my_hi, sh.warp_max[warp] = big;
+  }
   __syncthreads();
   if (tid == 0) {
-    uint64_t l = ~0ull, h = 0;
-    for (int i = 0; i < kSelWarps; ++i) l = min(l, range_lo[i]), h = max(h, range_hi[i]);
-    cta_lo = l, cta_hi = h;
+    uint64_t l = ~0u, h = 0;
+    uint32_t b = 0;
+    for (int i = 0; i < kSelWarps; ++i) {
+      l = min(l, sh.range_lo[i]), h = max(h, sh.range_hi[i]), b = max(b, sh.warp_max[i]);
+    }
+    sh.cta_lo = l, sh.cta_hi = h, sh.cta_max = b;
   }
   cluster.sync();
-  uint64_t lo = ~0ull, hi = 0;  // the active keys lie in [lo, hi]
+  uint32_t lo32 = ~0u, hi32 = 0, big = 0;  // the active keys lie in [lo32, hi32]
   for (uint32_t r = 0; r < nranks; ++r) {
-    lo = min(lo, *cluster.map_shared_rank(&cta_lo, r));
-    hi = max(hi, *cluster.map_shared_rank(&cta_hi, r));
+    const SelectShared* o = cluster.map_shared_rank(&sh, r);
+    lo32 = min(lo32, uint32_t(o->cta_lo));
+    hi32 = max(hi32, uint32_t(o->cta_hi));
+    big = max(big, o->cta_max);
+  }
+  const float err = Elem<TB>::to_float2(big).x * wsum * 0x1p-15f + 0x1p-117f;
+  const bool finite = big < (std::is_same<TB, __half>::value ? 0x7c00u : 0x7f80u) &&
+                      err < 0x1p126f && (wmax == 0.f || wmax >= 0x1p-126f);
+
+  // ---- the cut: keys above near_hi are kept, those below near_lo are not ----
+  int phase = 0;
+  bool exact = !finite;  // score every block in fp64
+  uint32_t near_lo = 0, near_hi = ~0u, active = need;
+  while (!exact) {
+    if (lo32 < hi32) {
+      const int shift = zoom(sh, cluster, keys32, count, lo32, hi32, active, phase);
+      phase ^= 1;
+      const uint32_t base = lo32 + (sh.found[0] << shift), width = (1u << shift) - 1u;
+      active -= sh.found[1];
+      lo32 = base;
+      if (width < hi32 - base) hi32 = base + width;
+    }
+    // the need-th largest fp32 score lies in [f_lo, f_hi]; the need-th largest
+    // score within err of it
+    const float f_lo = approx_value(lo32), f_hi = approx_value(hi32);
+    near_lo = lo32 ? approx_key(__fsub_rd(f_lo, 2.f * err)) : 0u;
+    near_hi = hi32 ? approx_key(__fadd_ru(f_hi, 2.f * err)) : 0u;
+    if (tid == 0) sh.above = sh.near = 0;
+    __syncthreads();
+    uint32_t n_above = 0;
+    for (int i = tid; i < count; i += kSelThreads) {
+      const uint32_t k = keys32[i];
+      n_above += k > near_hi;
+      if (k >= near_lo && k <= near_hi) {
+        const uint32_t at = atomicAdd(&sh.near, 1u);
+        if (at < kSelNear) sh.near_at[at] = i;
+      }
+    }
+    n_above = __reduce_add_sync(0xffffffffu, n_above);
+    if (lane == 0 && n_above) atomicAdd(&sh.above, n_above);
+    cluster.sync();
+    uint32_t near = 0, above = 0;
+    for (uint32_t r = 0; r < nranks; ++r) {
+      const SelectShared* o = cluster.map_shared_rank(&sh, r);
+      near += o->near, above += o->above;
+    }
+    if (near <= kSelNear || near + above == need) {
+      need -= above;
+      break;
+    }
+    // a range no wider than the doubt around it will not get better
+    exact = lo32 == hi32 || f_hi - f_lo <= err;
+    cluster.sync();  // above and near are written again
   }
 
-  // ---- threshold: keys above `hi` are kept, and the first `need` of those in
-  // [lo, hi], which are all of them or all equal. `found` is written again only
-  // after the next cluster.sync.
-  int phase = 0;
-  while (lo < hi) {
-    const uint64_t span = hi - lo;
-    const int bits = 64 - __clzll(static_cast<long long>(span));
-    const int shift = bits > kSelLog2Bins ? bits - kSelLog2Bins : 0;
-    uint32_t* mine = hist[phase];
-    for (int i = tid; i < count; i += kSelThreads) {
-      const uint64_t k = keys[i];
-      if (k >= lo && k <= hi) atomicAdd(&mine[uint32_t((k - lo) >> shift)], 1u);
+  uint64_t lo = 0, hi = 0;       // of the fp64 keys: those above hi are kept, and
+                                 // the first `need` of those in [lo, hi]
+  uint32_t cut = 0;              // of the fp32 keys: the least kept one
+  uint32_t base_gt = 0, base_eq = 0;  // kept / tied keys of the ranks before this one
+  if (!exact) {
+    uint32_t near = 0, before = 0, mine = sh.near;
+    for (uint32_t r = 0; r < nranks; ++r) {
+      const uint32_t o = cluster.map_shared_rank(&sh, r)->near;
+      if (r < rank) before += o;
+      near += o;
+    }
+    if (near == need) {  // every near block is kept
+      cut = near_lo;
+      if (tid < int(nranks)) sh.near_kept[tid] = cluster.map_shared_rank(&sh, tid)->near;
+      __syncthreads();
+    } else {
+      cut = near_hi + 1u;
+      for (uint32_t i = warp; i < mine; i += kSelWarps) {
+        const int at[1] = {int(sh.near_at[i])};
+        uint64_t k[1];
+        exact_keys<TB, D, 1>(a, weight, table, at, g, k);
+        if (lane == 0) sh.near_key[i] = k[0];
+      }
+      if (tid < 8) sh.near_kept[tid] = 0;
+      cluster.sync();
+      // each rank gathers all near keys and ranks them; position: rank, then place
+      uint32_t owner = 0, j = tid;
+      if (tid < int(near)) {
+        while (true) {
+          const uint32_t o = cluster.map_shared_rank(&sh, owner)->near;
+          if (j < o) break;
+          j -= o, ++owner;
+        }
+        const SelectShared* o = cluster.map_shared_rank(&sh, owner);
+        sh.all_key[tid] = o->near_key[j];
+        sh.all_at[tid] = owner * uint32_t(per) + o->near_at[j];
+      }
+      __syncthreads();
+      if (tid < int(near)) {
+        const uint64_t k = sh.all_key[tid];
+        const uint32_t at = sh.all_at[tid];
+        uint32_t better = 0;
+        for (uint32_t i = 0; i < near; ++i)
+          better += sh.all_key[i] > k || (sh.all_key[i] == k && sh.all_at[i] < at);
+        if (better < need) atomicAdd(&sh.near_kept[owner], 1u);
+        if (owner == rank) keys32[sh.near_at[j]] = better < need ? ~0u : 0u;
+      }
+      __syncthreads();
+    }
+    for (uint32_t r = 0; r < rank; ++r)
+      base_gt += cluster.map_shared_rank(&sh, r)->above + sh.near_kept[r];
+  } else {
+    cluster.sync();  // the scores and their range are written again
+    uint64_t my_lo = ~0ull, my_hi = 0;
+    constexpr int U = 8;  // blocks in flight per warp
+    for (int c0 = warp * U; c0 < count; c0 += kSelWarps * U) {
+      int at[U];
+      uint64_t k[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) at[u] = c0 + u < count ? c0 + u : -1;
+      exact_keys<TB, D, U>(a, weight, table, at, g, k);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (c0 + u >= count) continue;
+        if (lane == 0) keys[c0 + u] = k[u];
+        my_lo = min(my_lo, k[u]);
+        my_hi = max(my_hi, k[u]);
+      }
+    }
+    if (lane == 0) sh.range_lo[warp] = my_lo, sh.range_hi[warp] = my_hi;
+    __syncthreads();
+    if (tid == 0) {
+      for (int i = 1; i < kSelWarps; ++i)
+        my_lo = min(my_lo, sh.range_lo[i]), my_hi = max(my_hi, sh.range_hi[i]);
+      sh.cta_lo = my_lo, sh.cta_hi = my_hi;
     }
     cluster.sync();
-    // each thread: two neighbouring bins of the merged histogram, highest first
-    constexpr int PER = kSelBins / kSelThreads;
-    uint32_t bin[PER], total = 0;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      bin[j] = 0;
-      const int b = kSelBins - 1 - (tid * PER + j);
-      for (uint32_t r = 0; r < nranks; ++r) bin[j] += cluster.map_shared_rank(mine, r)[b];
-      total += bin[j];
+    lo = ~0ull, hi = 0;
+    for (uint32_t r = 0; r < nranks; ++r) {
+      const SelectShared* o = cluster.map_shared_rank(&sh, r);
+      lo = min(lo, o->cta_lo);
+      hi = max(hi, o->cta_hi);
     }
-    uint32_t incl = total;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, m);
-      if (lane >= m) incl += v;
+    while (lo < hi) {
+      const int shift = zoom(sh, cluster, keys, count, lo, hi, need, phase);
+      phase ^= 1;
+      need -= sh.found[1];
+      lo += uint64_t(sh.found[0]) << shift;
+      const uint64_t width = (uint64_t(1) << shift) - 1;
+      if (width < hi - lo) hi = lo + width;
+      if (sh.found[2] == need) break;  // the whole bin is kept
     }
-    if (lane == 31) warp_sum[warp] = incl;
-    // the other buffer was last read before this iteration's cluster.sync
-    for (int i = tid; i < kSelBins; i += kSelThreads) hist[phase ^ 1][i] = 0;
-    __syncthreads();
-    uint32_t above = incl - total;
-    for (int i = 0; i < warp; ++i) above += warp_sum[i];
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      if (above < need && above + bin[j] >= need)
-        found[0] = kSelBins - 1 - (tid * PER + j), found[1] = above, found[2] = bin[j];
-      above += bin[j];
-    }
-    __syncthreads();
-    const uint64_t base = lo + (uint64_t(found[0]) << shift);
-    need -= found[1];
-    lo = base;
-    const uint64_t width = (uint64_t(1) << shift) - 1;
-    if (width < hi - base) hi = base + width;
-    phase ^= 1;
-    if (found[2] == need) break;  // the whole bin is kept
   }
 
   // ---- kept blocks in ascending order ----
+  auto look = [&](int i, bool& gt, bool& eq) {
+    gt = eq = false;
+    if (i >= count) return;
+    if (exact) {
+      const uint64_t k = keys[i];
+      gt = k > hi;
+      eq = k >= lo && k <= hi;
+    } else {
+      gt = keys32[i] >= cut;
+    }
+  };
   const int chunk = ((count + kSelWarps - 1) / kSelWarps + 31) & ~31;
-  const int from = min(count, warp * chunk), to = min(count, from + chunk);
+  const int from = warp * chunk, to = min(count, from + chunk);
   uint32_t n_gt = 0, n_eq = 0;
-  for (int i = from + lane; i < from + chunk && i - lane < to; i += 32) {
-    const uint64_t k = i < to ? keys[i] : 0ull;
-    n_gt += __popc(__ballot_sync(0xffffffffu, i < to && k > hi));
-    n_eq += __popc(__ballot_sync(0xffffffffu, i < to && k >= lo && k <= hi));
+  for (int i = from; i < to; i += 32) {
+    bool gt, eq;
+    look(i + lane, gt, eq);
+    n_gt += __popc(__ballot_sync(0xffffffffu, gt));
+    n_eq += __popc(__ballot_sync(0xffffffffu, eq));
   }
-  if (lane == 0) take[0][warp] = n_gt, take[1][warp] = n_eq;
+  if (lane == 0) sh.take[0][warp] = n_gt, sh.take[1][warp] = n_eq;
   __syncthreads();
   if (tid < 2) {
     uint32_t sum = 0;
     for (int i = 0; i < kSelWarps; ++i) {
-      const uint32_t v = take[tid][i];
-      take[tid][i] = sum;
+      const uint32_t v = sh.take[tid][i];
+      sh.take[tid][i] = sum;
       sum += v;
     }
-    take[tid][kSelWarps] = sum;
+    sh.take[tid][kSelWarps] = sum;
   }
-  cluster.sync();
-  uint32_t gt = take[0][warp], eq = take[1][warp];
-  for (uint32_t r = 0; r < rank; ++r) {
-    gt += cluster.map_shared_rank(&take[0][0], r)[kSelWarps];
-    eq += cluster.map_shared_rank(&take[1][0], r)[kSelWarps];
+  if (exact) {
+    cluster.sync();
+    for (uint32_t r = 0; r < rank; ++r) {
+      const SelectShared* o = cluster.map_shared_rank(&sh, r);
+      base_gt += o->take[0][kSelWarps];
+      base_eq += o->take[1][kSelWarps];
+    }
   }
   cluster.sync();  // no CTA leaves while another reads its shared memory
-  for (int i = from + lane; i < from + chunk && i - lane < to; i += 32) {
-    const uint64_t k = i < to ? keys[i] : 0ull;
-    const uint32_t b_gt = __ballot_sync(0xffffffffu, i < to && k > hi);
-    const uint32_t b_eq = __ballot_sync(0xffffffffu, i < to && k >= lo && k <= hi);
+  uint32_t gt = base_gt + sh.take[0][warp], eq = base_eq + sh.take[1][warp];
+  for (int i = from; i < to; i += 32) {
+    bool is_gt, is_eq;
+    look(i + lane, is_gt, is_eq);
+    const uint32_t b_gt = __ballot_sync(0xffffffffu, is_gt);
+    const uint32_t b_eq = __ballot_sync(0xffffffffu, is_eq);
     const uint32_t below = (1u << lane) - 1u;
     const uint32_t my_eq = eq + __popc(b_eq & below);
-    const uint32_t at = a.sink + gt + __popc(b_gt & below) + min(my_eq, need);
-    if (((b_gt >> lane) & 1u) || (((b_eq >> lane) & 1u) && my_eq < need))
-      out[at] = a.sink + first + i;
+    const uint32_t at = a.sink + gt + __popc(b_gt & below) + (exact ? min(my_eq, need) : 0u);
+    if ((is_gt || (is_eq && my_eq < need)) && at < uint32_t(a.keep)) out[at] = a.sink + first + i + lane;
     gt += __popc(b_gt);
     eq += __popc(b_eq);
   }

@@ -24,7 +24,7 @@ template <typename Args>
 int launch_clusters(const char* fn, void (*kernel)(Args), int64_t units, int ranks, int threads,
                     int smem, int max_smem, const Args& args, cudaStream_t st) {
   if (units * ranks >= (int64_t(1) << 31)) return fail(KVP_ERR_INVALID, "%s: batch too large", fn);
-  if (smem > 40 * 1024) {  // with up to 8.5 KiB of static shared memory
+  if (smem > 32 * 1024) {  // beside up to 14 KiB of static shared memory
     cudaError_t e = ensure_smem(kernel, max_smem);
     if (e != cudaSuccess) return cuda_fail(e, fn);
   }
@@ -98,7 +98,7 @@ int launch_bounds(const kvp::dev::BoundsArgs& a, int64_t warps, cudaStream_t st)
   return e == cudaSuccess ? KVP_OK : cuda_fail(e, "update_key_bounds: launch");
 }
 
-// Scores kept per CTA of the selection (8 bytes each, beside 9 KiB of counters).
+// Scores kept per CTA of the selection (8 bytes each, beside 14 KiB of counters).
 constexpr int kSelMaxKeys = 26 * 1024;
 
 template <typename TQ, typename TB>
