@@ -12,7 +12,8 @@
 //
 // Bound by HBM (the context's bounds are read once) if the scores cost little:
 // in fp64 a block's 2 D conversions and multiply-adds and the reduction over the
-// lanes took 4.4 times as long as its bytes. So the scores are first taken on the
+// lanes took 4.4 times as long as its bytes (137 us for 32 x 8 rows of 1,500
+// blocks and D = 128; now 46, of them about 8 after the last byte). So the scores are first taken on the
 // tensor cores in fp32, 16 blocks (A rows) against the weights split into three
 // 16-bit parts (columns 0 to 2 of B), with a bound E on their error; only blocks
 // whose fp32 score lies within 2 E of the cut, usually a handful, are scored
@@ -27,11 +28,14 @@
 // twice.
 //
 // One cluster of up to 8 CTAs serves a (sequence, KV head); each CTA scores a
-// contiguous range of blocks and keeps the scores as order-preserving keys in
-// shared memory. The cut is found by zooming: a 1024-bin histogram of the active
-// key range, merged over the cluster through distributed shared memory, names
-// the bin that holds the last kept key. The kept blocks are written in ascending
-// order at offsets from a prefix sum over warps and CTAs.
+// contiguous range of blocks. The scores, as order-preserving keys, go straight to
+// the first CTA's shared memory, which selects alone: after the scores, what
+// counts is the latency of the steps, and a step over the cluster takes 2 to 4 us
+// (a barrier and remote reads) where one CTA takes under 1. Only a context with
+// more blocks than one CTA holds is selected by the cluster together. The cut is
+// found by zooming: a 1024-bin histogram of the active key range names the bin
+// that holds the last kept key. The kept blocks are written in ascending order at
+// offsets from a prefix sum over warps (and CTAs).
 #pragma once
 
 #include <cooperative_groups.h>
@@ -54,8 +58,7 @@ struct SelectArgs {
   int32_t keep, sink, recent;
 };
 
-constexpr int kSelWarps = 8;
-constexpr int kSelThreads = kSelWarps * 32;
+constexpr int kSelMaxWarps = 16;
 constexpr int kSelBins = 1024;
 constexpr int kSelLog2Bins = 10;
 constexpr int kSelNear = 64;  // most blocks near the cut that are scored again
@@ -75,46 +78,82 @@ __device__ __forceinline__ float approx_value(uint32_t k) {
   return __uint_as_float((k >> 31) ? (k ^ 0x80000000u) : ~k);
 }
 
-// The cluster's shared state of one selection.
+// Most CTAs of a cluster, and most keys of one CTA (8 bytes each).
+constexpr int kSelMaxRanks = 8;
+constexpr int kSelMaxKeys = 26 * 1024;
+
+// The shared state of one selection.
 struct SelectShared {
   uint32_t hist[2][kSelBins];
-  uint64_t range_lo[kSelWarps], range_hi[kSelWarps];
-  uint64_t cta_lo, cta_hi;       // range of the CTA's keys
-  uint32_t warp_max[kSelWarps], cta_max;  // largest |bound|, 16-bit pattern
-  uint32_t warp_sum[kSelWarps];
+  // of the keys of each warp of the CTAs that select together: range, and the
+  // largest |bound| (16-bit pattern)
+  uint32_t range_lo[kSelMaxRanks * kSelMaxWarps], range_hi[kSelMaxRanks * kSelMaxWarps];
+  uint32_t biggest[kSelMaxRanks * kSelMaxWarps];
+  uint64_t warp_lo[kSelMaxWarps], warp_hi[kSelMaxWarps], cta_lo, cta_hi;  // of the fp64 keys
+  uint32_t warp_sum[kSelMaxWarps];
+  float weight_max[kSelMaxWarps], weight_sum[kSelMaxWarps];
   uint32_t found[3];             // bin, keys above it, keys in it
-  uint32_t take[2][kSelWarps + 1];  // kept / tied keys per warp, and of the CTA
+  uint32_t take[2][kSelMaxWarps + 1];  // kept / tied keys per warp, and of the CTA
   uint32_t above, near;          // this CTA's keys past the near ones, near ones
   uint32_t near_at[kSelNear];    // their places, and fp64 keys
   uint64_t near_key[kSelNear];
-  uint32_t all_at[kSelNear];     // the cluster's, gathered
+  uint32_t all_at[kSelNear];     // all ranks', gathered
   uint64_t all_key[kSelNear];
-  uint32_t near_kept[8];         // kept near keys of each rank
+  uint32_t near_kept[kSelMaxRanks];  // kept near keys of each rank
 };
 
-// One zoom: the bin of keys[0, count) within [lo, hi] (over the cluster) that
-// holds the need-th largest, in found; hist[phase] is used, hist[phase ^ 1] is
-// cleared for the next. `found` is written again only after the next cluster.sync.
-template <typename Key, typename Cluster>
-__device__ __forceinline__ int zoom(SelectShared& sh, Cluster& cluster, const Key* keys, int count,
-                                    Key lo, Key hi, uint32_t need, int phase) {
+// The CTAs that select together: one (n = 1), or the whole cluster.
+struct SelectRanks {
+  cooperative_groups::cluster_group cluster;
+  uint32_t n;
+  __device__ __forceinline__ void sync() {
+    if (n == 1)
+      __syncthreads();
+    else
+      cluster.sync();
+  }
+  template <typename X>
+  __device__ __forceinline__ X* at(X* p, uint32_t r) {
+    return n == 1 ? p : cluster.map_shared_rank(p, r);
+  }
+};
+
+// f(i, keys[i]) for this thread's i of [0, count), eight reads in flight.
+template <int WARPS, typename Key, typename F>
+__device__ __forceinline__ void for_each_key(const Key* keys, int count, F f) {
+  constexpr int U = 8, kThreads = WARPS * 32;
+  for (int i0 = threadIdx.x; i0 < count; i0 += U * kThreads) {
+    Key k[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * kThreads < count) k[u] = keys[i0 + u * kThreads];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * kThreads < count) f(i0 + u * kThreads, k[u]);
+  }
+}
+
+// One zoom: the bin of keys[0, count) within [lo, hi] (over the ranks) that holds
+// the need-th largest, in found; hist[phase] is used, hist[phase ^ 1] is cleared
+// for the next. `found` is written again only after the next ranks.sync.
+template <int WARPS, typename Key>
+__device__ __forceinline__ int zoom(SelectShared& sh, SelectRanks& ranks, const Key* keys,
+                                    int count, Key lo, Key hi, uint32_t need, int phase) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t nranks = cluster.num_blocks();
   const int bits = 64 - __clzll(static_cast<long long>(hi - lo));
   const int shift = bits > kSelLog2Bins ? bits - kSelLog2Bins : 0;
   uint32_t* mine = sh.hist[phase];
-  for (int i = tid; i < count; i += kSelThreads) {
-    const Key k = keys[i];
+  for_each_key<WARPS>(keys, count, [&](int, Key k) {
     if (k >= lo && k <= hi) atomicAdd(&mine[uint32_t((k - lo) >> shift)], 1u);
-  }
-  cluster.sync();
+  });
+  ranks.sync();
   // each thread: neighbouring bins of the merged histogram, highest first
-  constexpr int PER = kSelBins / kSelThreads;
+  constexpr int PER = kSelBins / (WARPS * 32);
   uint32_t bin[PER], total = 0;
 #pragma unroll
   for (int j = 0; j < PER; ++j) bin[j] = 0;
-  for (uint32_t r = 0; r < nranks; ++r) {
-    const uint32_t* theirs = cluster.map_shared_rank(mine, r);
+  for (uint32_t r = 0; r < ranks.n; ++r) {
+    const uint32_t* theirs = ranks.at(mine, r);
 #pragma unroll
     for (int j = 0; j < PER; ++j) bin[j] += theirs[kSelBins - 1 - (tid * PER + j)];
   }
@@ -127,8 +166,8 @@ __device__ __forceinline__ int zoom(SelectShared& sh, Cluster& cluster, const Ke
     if (lane >= m) incl += v;
   }
   if (lane == 31) sh.warp_sum[warp] = incl;
-  // the other buffer was last read before this call's cluster.sync
-  for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[phase ^ 1][i] = 0;
+  // the other buffer was last read before this call's ranks.sync
+  for (int i = tid; i < kSelBins; i += WARPS * 32) sh.hist[phase ^ 1][i] = 0;
   __syncthreads();
   uint32_t above = incl - total;
   for (int i = 0; i < warp; ++i) above += sh.warp_sum[i];
@@ -178,18 +217,21 @@ __device__ __forceinline__ void exact_keys(const SelectArgs& a, const double* we
   }
 }
 
-// TQ: the queries' type, TB: the bounds' type.
-template <typename TQ, typename TB, int D>
-__global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const SelectArgs a) {
+// TQ: the queries' type, TB: the bounds' type, WARPS: per CTA.
+template <typename TQ, typename TB, int D, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
+    select_blocks_kernel(const SelectArgs a) {
   namespace cg = cooperative_groups;
+  constexpr int kThreads = WARPS * 32;
   extern __shared__ uint64_t keys[];
   uint32_t* keys32 = reinterpret_cast<uint32_t*>(keys);
   __shared__ SelectShared sh;
   __shared__ __align__(16) double weight[2 * D];    // Q+, then Q-
   __shared__ __align__(16) uint16_t part[3][2 * D]; // their scaled 16-bit parts
 
-  cg::cluster_group cluster = cg::this_cluster();
-  const uint32_t nranks = cluster.num_blocks(), rank = cluster.block_rank();
+  SelectRanks ranks{cg::this_cluster(), 1};
+  const uint32_t nranks = ranks.cluster.num_blocks();
+  uint32_t rank = ranks.cluster.block_rank();
   const uint32_t unit = blockIdx.x / nranks;
   const uint32_t s = unit / a.num_kv_heads, g = unit - s * a.num_kv_heads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -203,25 +245,67 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
   int32_t* out = a.out + int64_t(unit) * a.keep;
   if (n <= a.keep) {  // every block is kept (uniform over the cluster)
     if (rank == 0)
-      for (int i = tid; i < a.keep; i += kSelThreads) out[i] = i < n ? i : -1;
+      for (int i = tid; i < a.keep; i += kThreads) out[i] = i < n ? i : -1;
     return;
   }
   // n > keep >= sink + recent: candidates [sink, n - recent)
   const int cand = n - a.sink - a.recent;
   uint32_t need = a.keep - a.sink - a.recent;
   if (rank == 0) {
-    for (int i = tid; i < a.sink; i += kSelThreads) out[i] = i;
-    for (int i = tid; i < a.recent; i += kSelThreads) out[a.keep - a.recent + i] = n - a.recent + i;
+    for (int i = tid; i < a.sink; i += kThreads) out[i] = i;
+    for (int i = tid; i < a.recent; i += kThreads) out[a.keep - a.recent + i] = n - a.recent + i;
   }
   if (need == 0) return;
   const int per = (cand + nranks - 1) / nranks;
-  const int first = min(cand, int(rank) * per), count = min(cand, first + per) - first;
+  int first = min(cand, int(rank) * per), count = min(cand, first + per) - first;
   const int32_t* table = a.block_tables + int64_t(s) * a.max_blocks_per_seq + a.sink + first;
+  const bool gather = cand <= kSelMaxKeys;  // the first CTA selects alone
+
+  // the other CTAs' shared memory may be written once they have all started
+  if (nranks > 1) ranks.cluster.barrier_arrive();
+
+  // ---- the first loads of the scores, started beside the weights ----
+  // 16 blocks per warp and step: lane l holds rows r = l/4 and r + 8 of A and
+  // column r of B; of a row it reads 16 bytes at a time, whose words are the k
+  // positions of two MMA steps.
+  constexpr int ROW = 2 * D * 2;  // bytes of a block's bounds of one head
+  constexpr int L = ROW / 64;     // 16-byte loads per row and lane
+  const int r = lane >> 2, p = lane & 3;
+  auto locate = [&](int c0) {
+    int32_t id = -1;
+    const int c = c0 + (lane & 15);
+    if (c < count) {
+      id = __ldg(table + c);
+      if (id < 0 || id >= a.num_blocks) {
+        if (g == 0 && lane < 16)
+          record_error(KVP_DEVERR_BLOCK_ID, (uint64_t(s) << 32) | uint32_t(a.sink + first + c));
+        id = -1;
+      }
+    }
+    return id;
+  };
+  // a step's rows are loaded in two halves, each as soon as its registers are
+  // free, so that half of the bytes are always on the way
+  uint4 x[2][2][L / 2];
+  auto load = [&](int half, int32_t ids) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int32_t b = __shfl_sync(0xffffffffu, ids, r + 8 * y);
+      const char* src = static_cast<const char*>(a.bounds) +
+                        (int64_t(b) * a.num_kv_heads + g) * ROW + half * (ROW / 2) + p * 16;
+#pragma unroll
+      for (int j = 0; j < L / 2; ++j) {
+        x[half][y][j] = make_uint4(0, 0, 0, 0);
+        if (b >= 0) x[half][y][j] = ld_stream(src + j * 64);
+      }
+    }
+  };
+  int32_t id = locate(warp * 16), next = locate((warp + WARPS) * 16);
 
   // ---- weights: fp64 sums, and their three 16-bit parts ----
   const int G = a.num_q_heads / a.num_kv_heads;
   float wmax = 0.f, wsum = 0.f;
-  for (int e = tid; e < 2 * D; e += kSelThreads) {
+  for (int e = tid; e < 2 * D; e += kThreads) {
     const bool low = e >= D;
     const uint16_t* q = static_cast<const uint16_t*>(a.q) +
                         (int64_t(s) * a.num_q_heads + int64_t(g) * G) * D + (low ? e - D : e);
@@ -234,14 +318,16 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
     weight[e] = w;
     wmax = fmaxf(wmax, fabsf(float(w)));
   }
+  load(0, id);
+  load(1, id);
   for (int m = 1; m < 32; m <<= 1) wmax = fmaxf(wmax, __shfl_xor_sync(0xffffffffu, wmax, m));
-  if (lane == 0) sh.warp_sum[warp] = __float_as_uint(wmax);
-  for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[0][i] = 0;
+  if (lane == 0) sh.weight_max[warp] = wmax;
+  for (int i = tid; i < kSelBins; i += kThreads) sh.hist[0][i] = 0;
   __syncthreads();
-  for (int i = 0; i < kSelWarps; ++i) wmax = fmaxf(wmax, __uint_as_float(sh.warp_sum[i]));
+  for (int i = 0; i < WARPS; ++i) wmax = fmaxf(wmax, sh.weight_max[i]);
   const int wexp = int(__float_as_uint(wmax) >> 23) - 127;
   const double up = wmax > 0.f ? __hiloint2double((1023 + 14 - wexp) << 20, 0) : 1.0;
-  for (int e = tid; e < 2 * D; e += kSelThreads) {
+  for (int e = tid; e < 2 * D; e += kThreads) {
     double w = weight[e] * up;
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
@@ -252,19 +338,15 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
     wsum += float(fabs(weight[e] * up));
   }
   for (int m = 1; m < 32; m <<= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, m);
-  __syncthreads();
-  if (lane == 0) sh.warp_sum[warp] = __float_as_uint(wsum);
+  if (lane == 0) sh.weight_sum[warp] = wsum;
   __syncthreads();
   wsum = 0.f;
-  for (int i = 0; i < kSelWarps; ++i) wsum += __uint_as_float(sh.warp_sum[i]);
+  for (int i = 0; i < WARPS; ++i) wsum += sh.weight_sum[i];
 
-  // ---- fp32 scores: 16 blocks per warp and step ----
-  // Lane l holds rows r = l/4 and r + 8 of A and column r of B; of a row it reads
-  // 16 bytes at a time, whose words are the k positions of two MMA steps.
+  if (nranks > 1) ranks.cluster.barrier_wait();
+
+  // ---- fp32 scores ----
   {
-    constexpr int ROW = 2 * D * 2;  // bytes of a block's bounds of one head
-    constexpr int L = ROW / 64;     // 16-byte loads per row and lane
-    const int r = lane >> 2, p = lane & 3;
     uint4 w[L];
 #pragma unroll
     for (int j = 0; j < L; ++j) {
@@ -272,89 +354,79 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
       if (r < 3) w[j] = *reinterpret_cast<const uint4*>(&part[r][j * 32 + p * 8]);
     }
     uint32_t big = 0, my_lo = ~0u, my_hi = 0;
-    auto locate = [&](int c0) {
-      int32_t id = -1;
-      const int c = c0 + (lane & 15);
-      if (c < count) {
-        id = __ldg(table + c);
-        if (id < 0 || id >= a.num_blocks) {
-          if (g == 0 && lane < 16)
-            record_error(KVP_DEVERR_BLOCK_ID, (uint64_t(s) << 32) | uint32_t(a.sink + first + c));
-          id = -1;
-        }
-      }
-      return id;
-    };
-    int32_t id = locate(warp * 16);
-    for (int c0 = warp * 16; c0 < count; c0 += kSelWarps * 16) {
-      const int32_t b0 = __shfl_sync(0xffffffffu, id, r), b1 = __shfl_sync(0xffffffffu, id, r + 8);
-      uint4 x[2][L];
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int32_t b = y ? b1 : b0;
-        const char* src = static_cast<const char*>(a.bounds) +
-                          (int64_t(b) * a.num_kv_heads + g) * ROW + p * 16;
-#pragma unroll
-        for (int j = 0; j < L; ++j) {
-          x[y][j] = make_uint4(0, 0, 0, 0);
-          if (b >= 0) x[y][j] = ld_stream(src + j * 64);
-        }
-      }
-      id = locate(c0 + kSelWarps * 16);
+    uint32_t* dst = gather ? ranks.cluster.map_shared_rank(keys32, 0) + first : keys32;
+    for (int c0 = warp * 16; c0 < count; c0 += WARPS * 16) {
+      const int32_t after = locate(c0 + 2 * WARPS * 16);
       float z[2][4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) z[0][e] = z[1][e] = 0.f;
 #pragma unroll
-      for (int j = 0; j < L; ++j) {
-        const uint32_t a0[4] = {x[0][j].x, x[1][j].x, x[0][j].y, x[1][j].y};
-        const uint32_t a1[4] = {x[0][j].z, x[1][j].z, x[0][j].w, x[1][j].w};
-        mma16816<TB>(z[0], a0, w[j].x, w[j].y);
-        mma16816<TB>(z[1], a1, w[j].z, w[j].w);
+      for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          big = __vmaxu2(big, x[y][j].x & 0x7fff7fffu);
-          big = __vmaxu2(big, x[y][j].y & 0x7fff7fffu);
-          big = __vmaxu2(big, x[y][j].z & 0x7fff7fffu);
-          big = __vmaxu2(big, x[y][j].w & 0x7fff7fffu);
+        for (int j = 0; j < L / 2; ++j) {
+          const uint4 u = x[half][0][j], v = x[half][1][j], wj = w[half * (L / 2) + j];
+          const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
+          mma16816<TB>(z[0], a0, wj.x, wj.y);
+          mma16816<TB>(z[1], a1, wj.z, wj.w);
+          big = __vmaxu2(big, u.x & 0x7fff7fffu);
+          big = __vmaxu2(big, u.y & 0x7fff7fffu);
+          big = __vmaxu2(big, u.z & 0x7fff7fffu);
+          big = __vmaxu2(big, u.w & 0x7fff7fffu);
+          big = __vmaxu2(big, v.x & 0x7fff7fffu);
+          big = __vmaxu2(big, v.y & 0x7fff7fffu);
+          big = __vmaxu2(big, v.z & 0x7fff7fffu);
+          big = __vmaxu2(big, v.w & 0x7fff7fffu);
         }
+        load(half, next);
       }
       // columns 0 and 1 are in the lanes of p = 0, column 2 in those of p = 1
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const float c01 = (z[0][2 * y] + z[1][2 * y]) + (z[0][2 * y + 1] + z[1][2 * y + 1]);
         const float c2 = __shfl_down_sync(0xffffffffu, z[0][2 * y] + z[1][2 * y], 1);
+        const bool valid = __shfl_sync(0xffffffffu, id, r + 8 * y) >= 0;
         const int c = c0 + y * 8 + r;
         if (p == 0 && c < count) {
-          const uint32_t k = (y ? b1 : b0) >= 0 ? approx_key(c01 + c2) : 0u;
-          keys32[c] = k;
+          const uint32_t k = valid ? approx_key(c01 + c2) : 0u;
+          dst[c] = k;
           my_lo = min(my_lo, k);
           my_hi = max(my_hi, k);
         }
       }
+      id = next;
+      next = after;
     }
     big = max(big >> 16, big & 0xffffu);
     big = __reduce_max_sync(0xffffffffu, big);
     my_lo = __reduce_min_sync(0xffffffffu, my_lo);
     my_hi = __reduce_max_sync(0xffffffffu, my_hi);
-    if (lane == 0) sh.range_lo[warp] = my_lo, sh.range_hi[warp] = my_hi, sh.warp_max[warp] = big;
+    // to the first CTA, or to every one
+    if (lane == 0)
+      for (uint32_t o = 0; o < (gather ? 1 : nranks); ++o) {
+        SelectShared* to = ranks.cluster.map_shared_rank(&sh, o);
+        const int at = rank * WARPS + warp;
+        to->range_lo[at] = my_lo, to->range_hi[at] = my_hi, to->biggest[at] = big;
+      }
   }
-  __syncthreads();
-  if (tid == 0) {
-    uint64_t l = ~0u, h = 0;
-    uint32_t b = 0;
-    for (int i = 0; i < kSelWarps; ++i) {
-      l = min(l, sh.range_lo[i]), h = max(h, sh.range_hi[i]), b = max(b, sh.warp_max[i]);
-    }
-    sh.cta_lo = l, sh.cta_hi = h, sh.cta_max = b;
+  if (nranks > 1)
+    ranks.cluster.sync();
+  else
+    __syncthreads();
+  if (gather) {
+    if (rank != 0) return;  // nothing of this CTA's is read any more
+    count = cand;
+  } else {
+    ranks.n = nranks;
   }
-  cluster.sync();
   uint32_t lo32 = ~0u, hi32 = 0, big = 0;  // the active keys lie in [lo32, hi32]
-  for (uint32_t r = 0; r < nranks; ++r) {
-    const SelectShared* o = cluster.map_shared_rank(&sh, r);
-    lo32 = min(lo32, uint32_t(o->cta_lo));
-    hi32 = max(hi32, uint32_t(o->cta_hi));
-    big = max(big, o->cta_max);
+  for (int i = lane; i < int(nranks) * WARPS; i += 32) {
+    lo32 = min(lo32, sh.range_lo[i]);
+    hi32 = max(hi32, sh.range_hi[i]);
+    big = max(big, sh.biggest[i]);
   }
+  lo32 = __reduce_min_sync(0xffffffffu, lo32);
+  hi32 = __reduce_max_sync(0xffffffffu, hi32);
+  big = __reduce_max_sync(0xffffffffu, big);
   const float err = Elem<TB>::to_float2(big).x * wsum * 0x1p-15f + 0x1p-117f;
   const bool finite = big < (std::is_same<TB, __half>::value ? 0x7c00u : 0x7f80u) &&
                       err < 0x1p126f && (wmax == 0.f || wmax >= 0x1p-126f);
@@ -365,7 +437,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
   uint32_t near_lo = 0, near_hi = ~0u, active = need;
   while (!exact) {
     if (lo32 < hi32) {
-      const int shift = zoom(sh, cluster, keys32, count, lo32, hi32, active, phase);
+      const int shift = zoom<WARPS>(sh, ranks, keys32, count, lo32, hi32, active, phase);
       phase ^= 1;
       const uint32_t base = lo32 + (sh.found[0] << shift), width = (1u << shift) - 1u;
       active -= sh.found[1];
@@ -380,20 +452,19 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
     if (tid == 0) sh.above = sh.near = 0;
     __syncthreads();
     uint32_t n_above = 0;
-    for (int i = tid; i < count; i += kSelThreads) {
-      const uint32_t k = keys32[i];
+    for_each_key<WARPS>(keys32, count, [&](int i, uint32_t k) {
       n_above += k > near_hi;
       if (k >= near_lo && k <= near_hi) {
         const uint32_t at = atomicAdd(&sh.near, 1u);
         if (at < kSelNear) sh.near_at[at] = i;
       }
-    }
+    });
     n_above = __reduce_add_sync(0xffffffffu, n_above);
     if (lane == 0 && n_above) atomicAdd(&sh.above, n_above);
-    cluster.sync();
+    ranks.sync();
     uint32_t near = 0, above = 0;
-    for (uint32_t r = 0; r < nranks; ++r) {
-      const SelectShared* o = cluster.map_shared_rank(&sh, r);
+    for (uint32_t r = 0; r < ranks.n; ++r) {
+      const SelectShared* o = ranks.at(&sh, r);
       near += o->near, above += o->above;
     }
     if (near <= kSelNear || near + above == need) {
@@ -402,7 +473,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
     }
     // a range no wider than the doubt around it will not get better
     exact = lo32 == hi32 || f_hi - f_lo <= err;
-    cluster.sync();  // above and near are written again
+    ranks.sync();  // above and near are written again
   }
 
   uint64_t lo = 0, hi = 0;       // of the fp64 keys: those above hi are kept, and
@@ -411,34 +482,34 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
   uint32_t base_gt = 0, base_eq = 0;  // kept / tied keys of the ranks before this one
   if (!exact) {
     uint32_t near = 0, before = 0, mine = sh.near;
-    for (uint32_t r = 0; r < nranks; ++r) {
-      const uint32_t o = cluster.map_shared_rank(&sh, r)->near;
+    for (uint32_t r = 0; r < ranks.n; ++r) {
+      const uint32_t o = ranks.at(&sh, r)->near;
       if (r < rank) before += o;
       near += o;
     }
     if (near == need) {  // every near block is kept
       cut = near_lo;
-      if (tid < int(nranks)) sh.near_kept[tid] = cluster.map_shared_rank(&sh, tid)->near;
+      if (tid < int(ranks.n)) sh.near_kept[tid] = ranks.at(&sh, tid)->near;
       __syncthreads();
     } else {
       cut = near_hi + 1u;
-      for (uint32_t i = warp; i < mine; i += kSelWarps) {
+      for (uint32_t i = warp; i < mine; i += WARPS) {
         const int at[1] = {int(sh.near_at[i])};
         uint64_t k[1];
         exact_keys<TB, D, 1>(a, weight, table, at, g, k);
         if (lane == 0) sh.near_key[i] = k[0];
       }
-      if (tid < 8) sh.near_kept[tid] = 0;
-      cluster.sync();
+      if (tid < kSelMaxRanks) sh.near_kept[tid] = 0;
+      ranks.sync();
       // each rank gathers all near keys and ranks them; position: rank, then place
       uint32_t owner = 0, j = tid;
       if (tid < int(near)) {
         while (true) {
-          const uint32_t o = cluster.map_shared_rank(&sh, owner)->near;
+          const uint32_t o = ranks.at(&sh, owner)->near;
           if (j < o) break;
           j -= o, ++owner;
         }
-        const SelectShared* o = cluster.map_shared_rank(&sh, owner);
+        const SelectShared* o = ranks.at(&sh, owner);
         sh.all_key[tid] = o->near_key[j];
         sh.all_at[tid] = owner * uint32_t(per) + o->near_at[j];
       }
@@ -455,12 +526,12 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
       __syncthreads();
     }
     for (uint32_t r = 0; r < rank; ++r)
-      base_gt += cluster.map_shared_rank(&sh, r)->above + sh.near_kept[r];
+      base_gt += ranks.at(&sh, r)->above + sh.near_kept[r];
   } else {
-    cluster.sync();  // the scores and their range are written again
+    ranks.sync();  // the scores and their range are written again
     uint64_t my_lo = ~0ull, my_hi = 0;
     constexpr int U = 8;  // blocks in flight per warp
-    for (int c0 = warp * U; c0 < count; c0 += kSelWarps * U) {
+    for (int c0 = warp * U; c0 < count; c0 += WARPS * U) {
       int at[U];
       uint64_t k[U];
 #pragma unroll
@@ -474,22 +545,22 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
         my_hi = max(my_hi, k[u]);
       }
     }
-    if (lane == 0) sh.range_lo[warp] = my_lo, sh.range_hi[warp] = my_hi;
+    if (lane == 0) sh.warp_lo[warp] = my_lo, sh.warp_hi[warp] = my_hi;
     __syncthreads();
     if (tid == 0) {
-      for (int i = 1; i < kSelWarps; ++i)
-        my_lo = min(my_lo, sh.range_lo[i]), my_hi = max(my_hi, sh.range_hi[i]);
+      for (int i = 1; i < WARPS; ++i)
+        my_lo = min(my_lo, sh.warp_lo[i]), my_hi = max(my_hi, sh.warp_hi[i]);
       sh.cta_lo = my_lo, sh.cta_hi = my_hi;
     }
-    cluster.sync();
+    ranks.sync();
     lo = ~0ull, hi = 0;
-    for (uint32_t r = 0; r < nranks; ++r) {
-      const SelectShared* o = cluster.map_shared_rank(&sh, r);
+    for (uint32_t r = 0; r < ranks.n; ++r) {
+      const SelectShared* o = ranks.at(&sh, r);
       lo = min(lo, o->cta_lo);
       hi = max(hi, o->cta_hi);
     }
     while (lo < hi) {
-      const int shift = zoom(sh, cluster, keys, count, lo, hi, need, phase);
+      const int shift = zoom<WARPS>(sh, ranks, keys, count, lo, hi, need, phase);
       phase ^= 1;
       need -= sh.found[1];
       lo += uint64_t(sh.found[0]) << shift;
@@ -500,18 +571,46 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
   }
 
   // ---- kept blocks in ascending order ----
-  auto look = [&](int i, bool& gt, bool& eq) {
-    gt = eq = false;
-    if (i >= count) return;
-    if (exact) {
-      const uint64_t k = keys[i];
-      gt = k > hi;
-      eq = k >= lo && k <= hi;
-    } else {
-      gt = keys32[i] >= cut;
+  if (!exact) {
+    // a warp takes runs of 1024 keys in turn: lane i keeps the mask of the run's
+    // i-th 32 keys, so two scans (lanes, warps) give every mask its offset
+    ranks.sync();  // no CTA leaves, or reuses it, while another reads its memory
+    uint32_t at = a.sink + base_gt;
+    for (int c0 = 0; c0 < count; c0 += WARPS * 1024) {
+      const int from = c0 + warp * 1024;
+      uint32_t mask = 0;
+      const int masks = min(32, (count - from + 31) >> 5);
+#pragma unroll 8
+      for (int i = 0; i < masks; ++i) {
+        const int c = from + i * 32 + lane;
+        const uint32_t m = __ballot_sync(0xffffffffu, c < count && keys32[c] >= cut);
+        if (lane == i) mask = m;
+      }
+      uint32_t incl = __popc(mask);
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, m);
+        if (lane >= m) incl += v;
+      }
+      if (lane == 31) sh.warp_sum[warp] = incl;
+      __syncthreads();
+      uint32_t pos = at + incl - __popc(mask);
+      for (int i = 0; i < WARPS; ++i) {
+        if (i < warp) pos += sh.warp_sum[i];
+        at += sh.warp_sum[i];
+      }
+      for (; mask; mask &= mask - 1, ++pos)
+        if (pos < uint32_t(a.keep)) out[pos] = a.sink + first + from + lane * 32 + __ffs(mask) - 1;
+      __syncthreads();  // warp_sum is written again
     }
+    return;
+  }
+  auto look = [&](int i, bool& gt, bool& eq) {
+    const uint64_t k = i < count ? keys[i] : 0ull;
+    gt = i < count && k > hi;
+    eq = i < count && k >= lo && k <= hi;
   };
-  const int chunk = ((count + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int chunk = ((count + WARPS - 1) / WARPS + 31) & ~31;
   const int from = warp * chunk, to = min(count, from + chunk);
   uint32_t n_gt = 0, n_eq = 0;
   for (int i = from; i < to; i += 32) {
@@ -524,22 +623,20 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
   __syncthreads();
   if (tid < 2) {
     uint32_t sum = 0;
-    for (int i = 0; i < kSelWarps; ++i) {
+    for (int i = 0; i < WARPS; ++i) {
       const uint32_t v = sh.take[tid][i];
       sh.take[tid][i] = sum;
       sum += v;
     }
-    sh.take[tid][kSelWarps] = sum;
+    sh.take[tid][WARPS] = sum;
   }
-  if (exact) {
-    cluster.sync();
-    for (uint32_t r = 0; r < rank; ++r) {
-      const SelectShared* o = cluster.map_shared_rank(&sh, r);
-      base_gt += o->take[0][kSelWarps];
-      base_eq += o->take[1][kSelWarps];
-    }
+  ranks.sync();
+  for (uint32_t r = 0; r < rank; ++r) {
+    const SelectShared* o = ranks.at(&sh, r);
+    base_gt += o->take[0][WARPS];
+    base_eq += o->take[1][WARPS];
   }
-  cluster.sync();  // no CTA leaves while another reads its shared memory
+  ranks.sync();  // no CTA leaves while another reads its shared memory
   uint32_t gt = base_gt + sh.take[0][warp], eq = base_eq + sh.take[1][warp];
   for (int i = from; i < to; i += 32) {
     bool is_gt, is_eq;
@@ -548,7 +645,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_blocks_kernel(const Sel
     const uint32_t b_eq = __ballot_sync(0xffffffffu, is_eq);
     const uint32_t below = (1u << lane) - 1u;
     const uint32_t my_eq = eq + __popc(b_eq & below);
-    const uint32_t at = a.sink + gt + __popc(b_gt & below) + (exact ? min(my_eq, need) : 0u);
+    const uint32_t at = a.sink + gt + __popc(b_gt & below) + min(my_eq, need);
     if ((is_gt || (is_eq && my_eq < need)) && at < uint32_t(a.keep)) out[at] = a.sink + first + i + lane;
     gt += __popc(b_gt);
     eq += __popc(b_eq);

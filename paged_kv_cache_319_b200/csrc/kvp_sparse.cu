@@ -98,28 +98,31 @@ int launch_bounds(const kvp::dev::BoundsArgs& a, int64_t warps, cudaStream_t st)
   return e == cudaSuccess ? KVP_OK : cuda_fail(e, "update_key_bounds: launch");
 }
 
-// Scores kept per CTA of the selection (8 bytes each, beside 14 KiB of counters).
-constexpr int kSelMaxKeys = 26 * 1024;
-
 template <typename TQ, typename TB>
 int launch_select(const kvp::dev::SelectArgs& a, int head_dim, cudaStream_t st) {
+  using kvp::dev::kSelMaxKeys;
   const int64_t units = int64_t(a.num_seqs) * a.num_kv_heads;
   const int bs = 1 << a.log2_bs;
   const int blocks = int((int64_t(a.max_context_len) + bs - 1) / bs);
-  // more CTAs per row while the rows alone leave SMs idle and each still has 64 blocks
-  int ranks = 1;
-  while (ranks < 8 && ((units * ranks < 2 * sm_count() && blocks >= 128 * ranks) ||
-                       (blocks + ranks - 1) / ranks > kSelMaxKeys))
-    ranks *= 2;
-  const int per = (blocks + ranks - 1) / ranks;
-  if (per > kSelMaxKeys)
+  if (blocks > 8 * kSelMaxKeys)
     return fail(KVP_ERR_INVALID, "select_blocks: more than %d blocks per sequence", 8 * kSelMaxKeys);
-  const int smem = (per > 0 ? per : 1) * 8;
-  return head_dim == 128
-             ? launch_clusters("select_blocks", kvp::dev::select_blocks_kernel<TQ, TB, 128>, units,
-                               ranks, kvp::dev::kSelThreads, smem, kSelMaxKeys * 8, a, st)
-             : launch_clusters("select_blocks", kvp::dev::select_blocks_kernel<TQ, TB, 64>, units,
-                               ranks, kvp::dev::kSelThreads, smem, kSelMaxKeys * 8, a, st);
+  // one CTA holds every key, or each of eight its share
+  const bool gather = blocks <= kSelMaxKeys;
+  const int smem = gather ? (blocks > 0 ? blocks : 1) * 8 : kSelMaxKeys * 8;
+  // more CTAs per row while the rows alone leave SMs idle and each still has 128
+  // blocks (32 x 8 rows of 1,500 blocks: one CTA each 46 us, two 53, four 64)
+  int ranks = gather ? 1 : 8;
+  while (ranks < 8 && units * ranks < sm_count() && blocks >= 256 * ranks) ranks *= 2;
+  if (head_dim == 64)
+    return launch_clusters("select_blocks", kvp::dev::select_blocks_kernel<TQ, TB, 64, 8>, units,
+                           ranks, 256, smem, kSelMaxKeys * 8, a, st);
+  // one CTA per SM or fewer: twice the warps (8 rows of 8,192 blocks: 24.4 -> 20.9
+  // us; 16 CTAs per row do not all fit the GPCs at once: 24.0); else two CTAs per SM, so that one may load while one selects
+  return units * ranks <= sm_count() && blocks >= 256 * ranks
+             ? launch_clusters("select_blocks", kvp::dev::select_blocks_kernel<TQ, TB, 128, 16>,
+                               units, ranks, 512, smem, kSelMaxKeys * 8, a, st)
+             : launch_clusters("select_blocks", kvp::dev::select_blocks_kernel<TQ, TB, 128, 8>,
+                               units, ranks, 256, smem, kSelMaxKeys * 8, a, st);
 }
 
 template <typename T, bool FP8, int D, int NT>

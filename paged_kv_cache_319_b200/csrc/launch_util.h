@@ -40,7 +40,8 @@ int sm_count() {
   return n;
 }
 
-// Raises a kernel's dynamic shared-memory limit once per (kernel, device).
+// Raises a kernel's dynamic shared-memory limit once per (kernel, device), so
+// always to the same value.
 template <typename K>
 cudaError_t ensure_smem(K kernel, int bytes) {
   static std::mutex mu;

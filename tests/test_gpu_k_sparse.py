@@ -334,6 +334,33 @@ def test_selection_over_many_blocks_in_one_cluster():
         assert np.array_equal(got, np.sort(np.argsort(-vals, kind="stable")[:30]))
 
 
+@pytest.mark.parametrize("n,close", [(500, 500), (500, 20), (30000, 40), (30000, 30000), (3000, 65)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_selection_of_scores_closer_than_fp32_tells(n, close, dtype):
+    # every block scores 1024 + 2^-12 v, v one of 0..127 for `close` blocks (ties among
+    # them), 1104 for 10 blocks and 1000 for the rest; the cut falls among the close ones
+    kvp = _kvp()
+    rng = np.random.default_rng(44)
+    keep = 10 + close // 3
+    hi = np.zeros((n, 128))
+    hi[:, 0] = 1000
+    order = rng.permutation(n)
+    hi[order[:close], 0] = 1024
+    hi[order[:close], 1] = rng.integers(0, 128, close)
+    if close < n:
+        hi[order[close:close + 10], 0] = 1104
+    bounds = np.stack([hi, hi - 0.0], 1)[:, None]
+    q = np.zeros((1, 1, 128))
+    q[0, 0, 0], q[0, 0, 1] = 1.0, 2.0**-12
+    table = rng.permutation(n).astype(np.int32)[None]
+    got = kvp.select_blocks(_dev(q).to(_tdt(dtype)), _dev(bounds).to(_tdt(dtype)), _dev(table),
+                            _dev(np.int32([n * 16])), block_size=16, num_selected=keep,
+                            num_sink=0, num_recent=0)
+    kvp.check_device_error()
+    score = hi[table[0], 0] + 2.0**-12 * hi[table[0], 1]
+    assert np.array_equal(got.cpu().numpy()[0, 0], np.sort(np.argsort(-score, kind="stable")[:keep]))
+
+
 def test_selection_reports_bad_metadata():
     torch, kvp = _torch(), _kvp()
     bounds = torch.rand((20, 1, 2, 64), device="cuda").half()
