@@ -284,7 +284,12 @@ int update_key_bounds(const void* k_cache, void* key_bounds, const int32_t* bloc
   // n neighbouring tokens lie in (n + 2 bs - 2) / bs blocks at most
   const int64_t touched = (int64_t(a.max_new_tokens) + 2 * block_size - 2) / block_size;
   a.blocks_per_seq = int32_t(touched < all ? touched : all);
-  const int64_t warps = int64_t(num_seqs) * a.blocks_per_seq * num_kv_heads;
+  // several heads per warp once there are more tiles than 64 per SM
+  const int64_t tiles = int64_t(num_seqs) * a.blocks_per_seq * num_kv_heads;
+  const int64_t hpw = tiles / (int64_t(sm_count()) * 64);
+  a.heads_per_warp = int32_t(hpw < 1 ? 1 : hpw < num_kv_heads ? hpw : num_kv_heads);
+  a.head_groups = (num_kv_heads + a.heads_per_warp - 1) / a.heads_per_warp;
+  const int64_t warps = int64_t(num_seqs) * a.blocks_per_seq * a.head_groups;
   if (warps >= (int64_t(1) << 31) || int64_t(a.blocks_per_seq) * num_kv_heads >= (int64_t(1) << 31))
     return fail(KVP_ERR_INVALID, "%s: too many blocks in one call", fn);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
