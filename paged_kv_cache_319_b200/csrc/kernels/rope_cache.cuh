@@ -12,7 +12,10 @@
 // Bound by HBM: each of q, k and v is read once and written once. A CTA serves
 // one token; a thread owns 16 channels (both ends of 8 pairs) of every row it
 // visits, so its 8 cosines and 8 sines are loaded once and stay in registers
-// while it walks the token's heads.
+// while it walks the token's heads. 4 x 4,095 tokens of 32 + 8 heads into E4M3
+// (373 MB) take 67 us, 5.6 TB/s; what is left is the latency of slot, table row
+// and rows in turn. Four rows per thread in flight (80 registers) took 74 us, one
+// pass per CTA 77, CTAs that stay for many tokens 71.
 #pragma once
 
 #include "common.cuh"
