@@ -61,17 +61,16 @@ struct SparseArgs {
   float scale_log2;
 };
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 512;  // tiles located per pass over the list
 
-// Shared memory: per warp kStageBytes of K/V stages (later the merge area), then
-// the located rows and valid tokens of kChunk tiles' halves, then the barriers.
-// Two stages of 8 KiB (D = 128, 16-bit) or four of 4 KiB and three CTAs per SM:
-// a CTA's start and merge are covered by its neighbours' loads (64 sequences x 40
-// heads x 512 tokens: 108 us; two CTAs with three stages 124, one with six 182).
-constexpr int kStageBytes = 16 * 1024;
-constexpr int kSmemBytes = kWarps * kStageBytes + kChunk * 10 + kWarps * 16 * 8;
+// Shared memory: 64 KiB of K/V stages, shared out among the warps (later the merge
+// area), then the located rows and valid tokens of kChunk tiles' halves, then the
+// barriers. A warp has two stages of 8 KiB (D = 128, 16-bit; three CTAs of four
+// warps per SM: a CTA's start and merge are covered by its neighbours' loads. 64
+// sequences x 40 heads x 512 tokens: 108 us; two CTAs with three stages 124, one
+// with six 182) or, of tiles half as large, two stages of 4 KiB in twice the warps.
+constexpr int kStageBytes = 64 * 1024;
+constexpr int kSmemBytes = kStageBytes + kChunk * 10 + 8 * 16 * 8;
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
@@ -108,9 +107,15 @@ __device__ __forceinline__ uint32_t word(const uint4& x, int i) {
   return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
 }
 
+// Warps per CTA. The 16-head tiles' merge area leaves room for four.
+template <bool FP8, int D, int NT>
+constexpr int kSparseWarps = (FP8 || D == 64) && NT == 1 ? 8 : 4;
+
 // T: queries, output and products; FP8: E4M3 cache (D = 128); NT: tiles of 8 heads.
 template <typename T, bool FP8, int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) decode_sparse_kernel(const SparseArgs a) {
+__global__ void __launch_bounds__(kSparseWarps<FP8, D, NT> * 32,
+                                  kSparseWarps<FP8, D, NT> == 4 && NT == 1 ? 3 : 2)
+    decode_sparse_kernel(const SparseArgs a) {
   namespace cg = cooperative_groups;
   constexpr int ROW = D * (FP8 ? 1 : 2);  // bytes of a cached row
   constexpr int KL = ROW / 64;            // 16-byte key loads per token row and lane
@@ -125,8 +130,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) decode_sparse_kerne
   static_assert(!FP8 || D == 128, "E4M3 caches have head_dim 128");
 
   constexpr int TILE = 16 * ROW;                    // bytes of a tile's keys
-  constexpr int STAGES = kStageBytes / (2 * TILE);
-  static_assert(STAGES <= 16 && kWarps * kStageBytes >= (kWarps * HEADS * (D + 2) + 2 * HEADS) * 4,
+  constexpr int kWarps = kSparseWarps<FP8, D, NT>, kThreads = kWarps * 32;
+  constexpr int RING = kStageBytes / kWarps;  // bytes of a warp's stages
+  constexpr int STAGES = RING / (2 * TILE);
+  static_assert(STAGES <= 16 && kStageBytes >= (kWarps * HEADS * (D + 2) + 2 * HEADS) * 4,
                 "the merge area lies over the stages");
 
   extern __shared__ __align__(128) unsigned char smem[];
@@ -135,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) decode_sparse_kerne
   float* sm_l = sm_m + kWarps * HEADS;
   float* part_m = sm_l + kWarps * HEADS;              // [HEADS], this CTA's merged partial
   float* part_l = part_m + HEADS;
-  uint2* rows = reinterpret_cast<uint2*>(smem + kWarps * kStageBytes);  // [kChunk], a row per half
+  uint2* rows = reinterpret_cast<uint2*>(smem + kStageBytes);  // [kChunk], a row per half
   uint16_t* valid = reinterpret_cast<uint16_t*>(rows + kChunk);         // [kChunk], a byte per half
   uint64_t* bars = reinterpret_cast<uint64_t*>(valid + kChunk);         // [kWarps][16]
 
@@ -243,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) decode_sparse_kerne
   uint64_t* bar = bars + wid * 16;
   if (lane < STAGES) mbar_init(bar + lane, 1);
   fence_mbar_init();
-  const uint32_t stage0 = smem_u32(smem) + wid * kStageBytes;
+  const uint32_t stage0 = smem_u32(smem) + wid * RING;
   const uint64_t policy = l2_policy_evict_first();
   uint32_t phases = 0;  // parity of each stage's next completion
   bool alive = true;

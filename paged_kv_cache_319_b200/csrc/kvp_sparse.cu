@@ -132,11 +132,13 @@ int launch_sparse_nt(kvp::dev::sparse::SparseArgs a, cudaStream_t st) {
   a.head_tiles = (G + 8 * NT - 1) / (8 * NT);
   const int64_t units = int64_t(a.num_seqs) * a.num_kv_heads * a.head_tiles;
   const int64_t tiles = ((int64_t(a.num_selected) << a.log2_bs) + 15) / 16;
-  // more CTAs per row while the rows alone leave SMs idle and each warp still has 2 tiles
+  constexpr int warps = kSparseWarps<FP8, D, NT>;
+  // more CTAs per row while the rows alone leave SMs idle and each warp still has 2
+  // tiles (256 rows of 4,096 tokens: one CTA each 93 us, two 99, four 105)
   int ranks = 1;
-  while (ranks < 8 && units * ranks < 4 * sm_count() && tiles >= 4 * kWarps * ranks) ranks *= 2;
+  while (ranks < 8 && units * ranks < sm_count() && tiles >= 4 * warps * ranks) ranks *= 2;
   return launch_clusters("paged_attention_decode_sparse", decode_sparse_kernel<T, FP8, D, NT>,
-                         units, ranks, kThreads, kSmemBytes, kSmemBytes, a, st);
+                         units, ranks, warps * 32, kSmemBytes, kSmemBytes, a, st);
 }
 
 template <typename T, bool FP8, int D>
