@@ -714,19 +714,6 @@ KVP_API int paged_attention_decode_sparse(const void* q, const void* k_cache, co
                                           int32_t num_selected, float scale, void* out,
                                           int32_t dtype, int32_t cache_dtype, kvp_stream_t stream);
 
-/* One of the four calls above with its arguments in one block, for bindings that
- * pay for each argument of a foreign call (27 arguments took Python's ctypes 4.5
- * us, one block of them 1.2 us). words: num_words 64-bit words, one per argument
- * of the call in its order: a pointer or an integer as an int64_t, a float as a
- * double. A 32-bit argument whose word does not fit is refused.
- * Errors: those of the call, and KVP_ERR_INVALID (unknown call, words NULL,
- * num_words not the call's number of arguments). */
-#define KVP_CALL_ROPE_RESHAPE_AND_CACHE 0
-#define KVP_CALL_UPDATE_KEY_BOUNDS 1
-#define KVP_CALL_SELECT_BLOCKS 2
-#define KVP_CALL_DECODE_SPARSE 3
-KVP_API int kvp_call_words(int32_t call, const void* words, int32_t num_words);
-
 /* ---- virtually contiguous KV cache (CUDA virtual memory management) --------
  * The alternative the pages name to block tables: keep each sequence's cache
  * contiguous in virtual memory and back it with physical pages on demand

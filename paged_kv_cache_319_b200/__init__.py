@@ -1,9 +1,9 @@
 """Paged KV cache and decode attention for NVIDIA B200 (sm_100a).
 
-Python binding of libkvp (C ABI in ``include/kvp.h``). This module only
-marshals arguments: every step of the path - block bookkeeping, cache
+Python binding of libkvp (C ABI in ``include/kvp.h``). This module and its
+extension ``_torch_calls`` only marshal arguments: every step of the path - block bookkeeping, cache
 writes, copy-on-write copies, attention - runs in the native library. There
-is no Python or CPU fallback; calls fail loudly if ``libkvp.so`` is missing.
+is no Python or CPU fallback; calls fail loudly if a built library is missing.
 
 Host side: :class:`BlockPool` (fixed-size physical blocks, per-sequence block
 tables, allocation on growth, fork with refcounted copy-on-write, release).
@@ -17,13 +17,11 @@ for decoding over a part of a long context, :func:`rope_reshape_and_cache`,
 from __future__ import annotations
 
 import ctypes as C
-import struct
 
 import numpy as np
 
-from ._lib import (KVP_BF16, KVP_CALL_DECODE_SPARSE, KVP_CALL_ROPE_RESHAPE_AND_CACHE,
-                   KVP_CALL_SELECT_BLOCKS, KVP_CALL_UPDATE_KEY_BOUNDS, KVP_F16, KVP_FP8_E4M3,
-                   KvpError, P_i32, P_i64, PoolStats, VCacheStats, check, lib)
+from ._lib import (KVP_BF16, KVP_F16, KVP_FP8_E4M3, KvpError, P_i32, P_i64, PoolStats,
+                   VCacheStats, check, lib)
 
 __all__ = [
     "BlockPool", "KvpError", "reshape_and_cache", "copy_blocks", "paged_attention_decode",
@@ -672,101 +670,22 @@ def attention_decode_vcache(q, vc: VCache, seq_slots, context_lens, scale: float
     return out
 
 
-# The calls below take their arguments in one block (``kvp_call_words``): per argument
-# that is a fraction of what ctypes takes, and these calls run once per layer and step.
-_ROPE, _BOUNDS, _SELECT, _SPARSE, _WORD = (struct.Struct(f) for f in
-                                           ("26q", "14q", "18q", "17qd3q", "q"))
+_calls_module = None
 
 
-def _index(*ts) -> int:
-    """The index of the CUDA device that all of ``ts``, contiguous, are on."""
-    idx = ts[0].get_device()
-    for t in ts:
-        if t.get_device() != idx or not t.is_contiguous():
-            _cuda(*ts)
-    if idx < 0:
-        _cuda(*ts)
-    return idx
-
-
-def _call(idx: int, call: int, words: bytes, num_words: int) -> None:
-    """Entry point ``call`` with ``words`` and, as the last one, the current stream of
-    device ``idx``, with that device current."""
-    torch = _torch()
-    if torch.cuda.current_device() == idx:
-        words += _WORD.pack(torch._C._cuda_getCurrentRawStream(idx))
-        rc = lib().kvp_call_words(call, words, num_words)
-    else:
-        with torch.cuda.device(idx):
-            words += _WORD.pack(torch._C._cuda_getCurrentRawStream(idx))
-            rc = lib().kvp_call_words(call, words, num_words)
-    if rc:
-        check(rc)
-
-
-_codes_of = {}  # torch dtype -> element type of a pool
-
-
-def _codes() -> dict:
-    if not _codes_of:
-        torch = _torch()
-        _codes_of.update({torch.float16: KVP_F16, torch.bfloat16: KVP_BF16,
-                          torch.uint8: KVP_FP8_E4M3, torch.float8_e4m3fn: KVP_FP8_E4M3})
-    return _codes_of
-
-
-def _types(rows, k_cache, v_cache) -> tuple[int, int]:
-    """Element types of 16-bit rows and of pools beside them: the same, or E4M3."""
-    codes = _codes()
-    dtype, kt = rows.dtype, k_cache.dtype
-    code, cache = codes.get(dtype), codes.get(kt)
-    if v_cache.dtype != kt or code is None or code == KVP_FP8_E4M3:
-        raise TypeError("16-bit rows and caches of one dtype are needed")
-    if cache != code and cache != KVP_FP8_E4M3:
-        raise TypeError("the caches must have the dtype of the rows, or be E4M3")
-    return code, cache
-
-
-def _scale_ptrs(k_scale, v_scale, cache_code, Hkv, idx):
-    """Pointers of an E4M3 cache's scales; a 16-bit cache has none."""
-    if cache_code != KVP_FP8_E4M3:
-        if k_scale is not None or v_scale is not None:
-            raise ValueError("k_scale / v_scale belong to E4M3 caches")
-        return 0, 0
-    if k_scale is None or v_scale is None:
-        raise ValueError("an E4M3 cache needs k_scale and v_scale")
-    f32 = _torch().float32
-    if (k_scale.dtype != f32 or v_scale.dtype != f32 or k_scale.shape != (Hkv,) or
-            v_scale.shape != (Hkv,) or _index(k_scale, v_scale) != idx):
-        raise ValueError("k_scale / v_scale must be CUDA float32 [num_kv_heads] on the cache's device")
-    return k_scale.data_ptr(), v_scale.data_ptr()
-
-
-def _rows(x, idx: int, T: int, H: int, D: int, dtype) -> int:
-    """Checks ``x [T, H, D]`` of ``dtype`` on device ``idx``, each token's heads
-    contiguous; the elements between two tokens."""
-    if x.get_device() != idx:
-        raise ValueError("all tensors must be on the same CUDA device")
-    if x.dtype != dtype:
-        raise TypeError("dtype mismatch")
-    if x.shape != (T, H, D):
-        raise ValueError("shape mismatch")
-    st, sh, sd = x.stride()
-    if T and ((sd != 1 and D > 1) or (sh != D and H > 1)):
-        raise ValueError("the heads of a token must be contiguous")
-    return st if T > 1 else H * D
-
-
-def _tables_lens(block_tables, context_lens, S: int, bs: int, max_context_len) -> tuple[int, int]:
-    """Checks the batch metadata; (max_blocks_per_seq, max_context_len)."""
-    i32 = _torch().int32
-    if block_tables.dtype != i32 or context_lens.dtype != i32:
-        raise TypeError("block_tables and context_lens must be int32")
-    S2, MB = block_tables.shape
-    L, = context_lens.shape
-    if S2 != S or L != S:
-        raise ValueError("batch metadata mismatch")
-    return MB or 1, min(MB * bs, 2**31 - 1) if max_context_len is None else int(max_context_len)
+def _calls():
+    """The extension that checks and passes the tensors of the calls below; it has to be
+    built, there is no other way in."""
+    global _calls_module
+    if _calls_module is None:
+        try:
+            from . import _torch_calls
+        except ImportError as e:
+            raise RuntimeError("_torch_calls.so is missing or does not load; build it with "
+                               "`python -m paged_kv_cache_319_b200.build`") from e
+        _torch_calls.init(_torch().Tensor)
+        _calls_module = _torch_calls
+    return _calls_module
 
 
 def rope_reshape_and_cache(q, k_new, v_new, cos_sin, positions, k_cache, v_cache, slot_mapping,
@@ -780,34 +699,12 @@ def rope_reshape_and_cache(q, k_new, v_new, cos_sin, positions, k_cache, v_cache
     output); ``q_out`` may be ``q`` itself. The caches are of the rows' dtype, or E4M3
     with ``k_scale`` and ``v_scale`` as for :func:`reshape_and_cache_fp8`. A negative
     slot stores nothing; a negative position with it leaves the row of ``q_out`` too."""
-    torch = _torch()
-    idx = _index(k_cache, v_cache, cos_sin, positions, slot_mapping)
-    code, cache_code = _types(q, k_cache, v_cache)
-    dtype, pool = q.dtype, k_cache.shape
-    NB, Hkv, bs, D = pool
-    T, Hq, _ = q.shape
-    far, rot = cos_sin.shape
-    T2, = positions.shape
-    T3, = slot_mapping.shape
-    if v_cache.shape != pool or T2 != T or T3 != T:
-        raise ValueError("shape mismatch")
-    if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int64:
-        raise TypeError("positions and slot_mapping must be int64")
-    if cos_sin.dtype != torch.float32:
-        raise TypeError("cos_sin must be float32 [max_positions, rot_dim]")
-    q_stride = _rows(q, idx, T, Hq, D, dtype)
-    k_stride = _rows(k_new, idx, T, Hkv, D, dtype)
-    v_stride = _rows(v_new, idx, T, Hkv, D, dtype)
     if q_out is None:
-        q_out, o_stride = q.new_empty((T, Hq, D)), Hq * D
-    else:
-        o_stride = _rows(q_out, idx, T, Hq, D, dtype)
-    ks, vs = _scale_ptrs(k_scale, v_scale, cache_code, Hkv, idx)
-    _call(idx, KVP_CALL_ROPE_RESHAPE_AND_CACHE,
-          _ROPE.pack(q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), q_out.data_ptr(), q_stride,
-                     k_stride, v_stride, o_stride, cos_sin.data_ptr(), positions.data_ptr(), far,
-                     rot, 1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(),
-                     slot_mapping.data_ptr(), ks, vs, T, Hq, Hkv, D, bs, NB, code, cache_code), 27)
+        q_out = q.new_empty(q.shape)
+    rc = _calls().rope_reshape_and_cache(q, k_new, v_new, cos_sin, positions, k_cache, v_cache,
+                                         slot_mapping, q_out, interleaved, k_scale, v_scale)
+    if rc:
+        check(rc)
     return q_out
 
 
@@ -821,28 +718,10 @@ def update_key_bounds(k_cache, key_bounds, block_tables, context_lens, *, new_to
     ``max_new_tokens`` bounds the entries of ``new_tokens`` (default: the context's
     bound). The bounds have the cache's dtype, or float16 (the codes' values) over an
     E4M3 cache."""
-    torch = _torch()
-    idx = _index(k_cache, key_bounds, block_tables, context_lens)
-    NB, Hkv, bs, D = k_cache.shape
-    code = _codes().get(k_cache.dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {k_cache.dtype}")
-    if key_bounds.shape != (NB, Hkv, 2, D):
-        raise ValueError("key_bounds must be [NB, Hkv, 2, D]")
-    if key_bounds.dtype != (torch.float16 if code == KVP_FP8_E4M3 else k_cache.dtype):
-        raise TypeError("key_bounds must have the cache's dtype (float16 over an E4M3 cache)")
-    S, _ = block_tables.shape
-    MB, mcl = _tables_lens(block_tables, context_lens, S, bs, max_context_len)
-    new_ptr = 0
-    if new_tokens is not None:
-        if (new_tokens.dtype != torch.int32 or new_tokens.shape != (S,) or
-                _index(new_tokens) != idx):
-            raise ValueError("new_tokens must be CUDA int32 [S] on the cache's device")
-        new_ptr = new_tokens.data_ptr()
-    most = mcl if max_new_tokens is None else int(max_new_tokens)
-    _call(idx, KVP_CALL_UPDATE_KEY_BOUNDS,
-          _BOUNDS.pack(k_cache.data_ptr(), key_bounds.data_ptr(), block_tables.data_ptr(),
-                       context_lens.data_ptr(), new_ptr, S, Hkv, D, bs, NB, MB, mcl, most, code), 15)
+    rc = _calls().update_key_bounds(k_cache, key_bounds, block_tables, context_lens, new_tokens,
+                                    max_new_tokens, max_context_len)
+    if rc:
+        check(rc)
 
 
 def select_blocks(q, key_bounds, block_tables, context_lens, out=None, *, block_size: int,
@@ -854,29 +733,12 @@ def select_blocks(q, key_bounds, block_tables, context_lens, out=None, *, block_
     The first ``num_sink`` and last ``num_recent`` blocks are always kept, the others by an
     upper bound on the group's logits from ``key_bounds`` (see :func:`update_key_bounds`);
     a context of at most ``num_selected`` blocks keeps them all."""
-    torch = _torch()
-    idx = _index(q, key_bounds, block_tables, context_lens)
-    S, Hq, D = q.shape
-    NB, Hkv, two, D2 = key_bounds.shape
-    if two != 2 or D2 != D:
-        raise ValueError("key_bounds must be [NB, Hkv, 2, D]")
-    code, cache_code = _codes().get(q.dtype), _codes().get(key_bounds.dtype)
-    if code is None or code == KVP_FP8_E4M3 or cache_code is None:
-        raise TypeError(f"unsupported dtype {q.dtype}")
-    if cache_code != code:
-        if cache_code != KVP_F16:
-            raise TypeError("key_bounds must have q's dtype, or float16 (bounds of an E4M3 cache)")
-        cache_code = KVP_FP8_E4M3
-    bs, keep = int(block_size), int(num_selected)
-    MB, mcl = _tables_lens(block_tables, context_lens, S, bs, max_context_len)
     if out is None:
-        out = context_lens.new_empty((S, Hkv, max(keep, 0)))
-    elif _index(out) != idx or out.dtype != torch.int32 or out.shape != (S, Hkv, keep):
-        raise ValueError("out must be CUDA int32 [S, Hkv, num_selected]")
-    _call(idx, KVP_CALL_SELECT_BLOCKS,
-          _SELECT.pack(q.data_ptr(), key_bounds.data_ptr(), block_tables.data_ptr(),
-                       context_lens.data_ptr(), out.data_ptr(), S, Hq, Hkv, D, bs, NB, MB, mcl, keep,
-                       int(num_sink), int(num_recent), code, cache_code), 19)
+        out = context_lens.new_empty((q.shape[0], key_bounds.shape[1], max(num_selected, 0)))
+    rc = _calls().select_blocks(q, key_bounds, block_tables, context_lens, out, block_size,
+                                num_selected, num_sink, num_recent, max_context_len)
+    if rc:
+        check(rc)
     return out
 
 
@@ -888,28 +750,13 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, block_tables, context_len
 
     The caches are of q's dtype, or E4M3 with ``k_scale`` and ``v_scale`` (CUDA float32
     ``[Hkv]``). A row whose list leaves no token is zero."""
-    torch = _torch()
-    idx = _index(q, k_cache, v_cache, block_tables, context_lens, selected)
-    code, cache_code = _types(q, k_cache, v_cache)
-    S, Hq, D = q.shape
-    pool = k_cache.shape
-    NB, Hkv, bs, D2 = pool
-    S2, Hkv2, keep = selected.shape
-    if D2 != D or v_cache.shape != pool:
-        raise ValueError("q / cache mismatch")
-    if selected.dtype != torch.int32 or S2 != S or Hkv2 != Hkv:
-        raise ValueError("selected must be int32 [S, Hkv, n]")
-    MB, mcl = _tables_lens(block_tables, context_lens, S, bs, max_context_len)
-    ks, vs = _scale_ptrs(k_scale, v_scale, cache_code, Hkv, idx)
     if out is None:
-        out = torch.empty_like(q)
-    elif out.dtype != q.dtype or out.shape != q.shape or _index(out) != idx:
-        raise ValueError("out mismatch")
-    _call(idx, KVP_CALL_DECODE_SPARSE,
-          _SPARSE.pack(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs,
-                       block_tables.data_ptr(), context_lens.data_ptr(), selected.data_ptr(), S, Hq,
-                       Hkv, D, bs, NB, MB, mcl, keep, float(scale), out.data_ptr(), code,
-                       cache_code), 22)
+        out = _torch().empty_like(q)
+    rc = _calls().paged_attention_decode_sparse(q, k_cache, v_cache, block_tables, context_lens,
+                                                selected, scale, out, k_scale, v_scale,
+                                                max_context_len)
+    if rc:
+        check(rc)
     return out
 
 

@@ -18,11 +18,6 @@ KVP_ERR_CAPACITY = -6
 KVP_F16 = 0
 KVP_BF16 = 1
 KVP_FP8_E4M3 = 2
-
-KVP_CALL_ROPE_RESHAPE_AND_CACHE = 0
-KVP_CALL_UPDATE_KEY_BOUNDS = 1
-KVP_CALL_SELECT_BLOCKS = 2
-KVP_CALL_DECODE_SPARSE = 3
 KVP_STATIC_SCRATCH_BYTES = 40 * 1024 * 1024  # include/kvp.h
 
 ERROR_KINDS = {
@@ -131,7 +126,6 @@ SIGNATURES = {
                                 i32, i32, i32, i32, vp]),
     "paged_attention_decode_sparse": (C.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32,
                                                 i32, i32, i32, i32, i32, f32, vp, i32, i32, vp]),
-    "kvp_call_words": (C.c_int, [i32, C.c_char_p, i32]),
     "kvp_check_device_error": (C.c_int, [vp]),
     "kvp_selftest_bounded_wait": (C.c_int, [i32, vp]),
     "kvp_last_error_message": (C.c_char_p, []),

@@ -1,7 +1,8 @@
-"""Builds libkvp.so in place (sm_100a) with nvcc.
+"""Builds libkvp.so (sm_100a) and _torch_calls.so, the Python extension that passes
+torch tensors to it, in place with nvcc.
 
 Usage: ``python -m paged_kv_cache_319_b200.build [--force] [--verbose]``.
-The library lands next to this file so the package loads it from the source
+They land next to this file so the package loads them from the source
 tree; intermediate output (the ptxas report) goes to ``_build/``.
 """
 
@@ -9,16 +10,20 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkvp.so")
+CALLS = os.path.join(PKG, "_torch_calls.so")
+CALLS_SOURCE = os.path.join(CSRC, "host", "torch_calls.cpp")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = [
@@ -40,9 +45,9 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -76,12 +81,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
         link = [nvcc()] + flags + ["-shared", "-o", tmp] + objects
         res = subprocess.run(link, capture_output=True, text=True)
         cmds, out, failed = cmds + [link], out + res.stdout + res.stderr, res.returncode != 0
+    if not failed:
+        os.replace(tmp, LIB)
+        # torch is needed for one header, DLPack's
+        torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+        link = [nvcc(), "-std=c++17", "-O3", "-gencode", "arch=compute_100a,code=sm_100a",
+                "-Xcompiler", "-fPIC,-O3,-fvisibility=hidden", "-I", INCLUDE,
+                "-I", os.path.join(torch_dir, "include"), "-I", sysconfig.get_paths()["include"],
+                "-shared", "-o", CALLS + ".tmp", CALLS_SOURCE, "-L", PKG, "-l:libkvp.so",
+                "-Xlinker", "-rpath", "-Xlinker", "$ORIGIN"]
+        res = subprocess.run(link, capture_output=True, text=True)
+        cmds, out, failed = cmds + [link], out + res.stdout + res.stderr, res.returncode != 0
     with open(os.path.join(BUILD_DIR, "nvcc.log"), "w") as f:
         f.write("\n".join(" ".join(c) for c in cmds) + "\n\n" + out)
     if failed:
         sys.stderr.write(out)
         raise RuntimeError("nvcc failed; see " + os.path.join(BUILD_DIR, "nvcc.log"))
-    os.replace(tmp, LIB)
+    os.replace(CALLS + ".tmp", CALLS)
     if verbose:
         sys.stdout.write(out)
     return LIB

@@ -6,7 +6,6 @@
 
 #include <cmath>
 #include <cstdint>
-#include <cstring>
 
 #include "kernels/common.cuh"
 #include "kernels/decode_sparse.cuh"
@@ -396,67 +395,6 @@ int paged_attention_decode_sparse(const void* q, const void* k_cache, const void
                             : launch_sparse<__nv_bfloat16, false, 128>(a, st);
   return dtype == KVP_F16 ? launch_sparse<__half, false, 64>(a, st)
                           : launch_sparse<__nv_bfloat16, false, 64>(a, st);
-}
-
-int kvp_call_words(int32_t call, const void* words, int32_t num_words) {
-  const char* fn = "kvp_call_words";
-  static const int32_t counts[] = {27, 15, 19, 22};
-  if (call < 0 || call > KVP_CALL_DECODE_SPARSE) return fail(KVP_ERR_INVALID, "%s: unknown call", fn);
-  if (!words || num_words != counts[call])
-    return fail(KVP_ERR_INVALID, "%s: %d words expected", fn, counts[call]);
-  const char* w = static_cast<const char*>(words);
-  bool fits = true;
-  auto wide = [&](int i) {
-    int64_t x;
-    memcpy(&x, w + 8 * i, 8);
-    return x;
-  };
-  auto ptr = [&](int i) { return reinterpret_cast<void*>(static_cast<intptr_t>(wide(i))); };
-  auto i32 = [&](int i) {
-    const int64_t x = wide(i);
-    fits = fits && x == int32_t(x);
-    return int32_t(x);
-  };
-  auto f32 = [&](int i) {
-    double x;
-    memcpy(&x, w + 8 * i, 8);
-    return float(x);
-  };
-  auto cf = [&](int i) { return static_cast<const float*>(ptr(i)); };
-  auto ci = [&](int i) { return static_cast<const int32_t*>(ptr(i)); };
-  auto cl = [&](int i) { return static_cast<const int64_t*>(ptr(i)); };
-  int32_t n[16];  // the call's 32-bit arguments from word `first` on
-  auto ints = [&](int first, int count) {
-    for (int i = 0; i < count; ++i) n[i] = i32(first + i);
-    return fits;
-  };
-  switch (call) {
-    case KVP_CALL_ROPE_RESHAPE_AND_CACHE: {
-      const int32_t rot_dim = i32(11), interleaved = i32(12);
-      if (!ints(18, 8)) break;
-      return rope_reshape_and_cache(ptr(0), ptr(1), ptr(2), ptr(3), wide(4), wide(5), wide(6),
-                                    wide(7), cf(8), cl(9), wide(10), rot_dim, interleaved, ptr(13),
-                                    ptr(14), cl(15), cf(16), cf(17), n[0], n[1], n[2], n[3], n[4],
-                                    n[5], n[6], n[7], ptr(26));
-    }
-    case KVP_CALL_UPDATE_KEY_BOUNDS:
-      if (!ints(5, 9)) break;
-      return update_key_bounds(ptr(0), ptr(1), ci(2), ci(3), ci(4), n[0], n[1], n[2], n[3], n[4],
-                               n[5], n[6], n[7], n[8], ptr(14));
-    case KVP_CALL_SELECT_BLOCKS:
-      if (!ints(5, 13)) break;
-      return select_blocks(ptr(0), ptr(1), ci(2), ci(3), static_cast<int32_t*>(ptr(4)), n[0], n[1],
-                           n[2], n[3], n[4], n[5], n[6], n[7], n[8], n[9], n[10], n[11], n[12],
-                           ptr(18));
-    default: {
-      const int32_t dtype = i32(19), cache_dtype = i32(20);
-      if (!ints(8, 9)) break;
-      return paged_attention_decode_sparse(ptr(0), ptr(1), ptr(2), cf(3), cf(4), ci(5), ci(6),
-                                           ci(7), n[0], n[1], n[2], n[3], n[4], n[5], n[6], n[7],
-                                           n[8], f32(17), ptr(18), dtype, cache_dtype, ptr(21));
-    }
-  }
-  return fail(KVP_ERR_INVALID, "%s: a 32-bit argument is out of range", fn);
 }
 
 }  // extern "C"

@@ -2,7 +2,6 @@
 KVP_ERR_INVALID before any CUDA call. The pointers are fake and never dereferenced."""
 
 import ctypes as C
-import struct
 
 import pytest
 
@@ -34,21 +33,9 @@ DECODE = dict(q=p(1), k=p(2), v=p(3), kscale=None, vscale=None, t=p(4), l=p(5), 
               st=None)
 
 
-def words(args):
-    """The arguments as 64-bit words: pointers and integers, floats as doubles."""
-    vals = [(a.value or 0) if isinstance(a, C.c_void_p) else 0 if a is None else a for a in args]
-    return struct.pack("".join("d" if isinstance(v, float) else "q" for v in vals), *vals)
-
-
 def call(fn, base, **kw):
-    """The entry point's status, the same for the plain and the one-block call."""
     assert set(kw) <= set(base)
-    args = list({**base, **kw}.values())
-    rc = fn(*args)
-    code = ("rope_reshape_and_cache", "update_key_bounds", "select_blocks",
-            "paged_attention_decode_sparse").index(fn.__name__)
-    assert _lib.lib().kvp_call_words(code, words(args), len(args)) == rc
-    return rc
+    return fn(*{**base, **kw}.values())
 
 
 @pytest.mark.parametrize("bad", [
@@ -103,13 +90,19 @@ def test_empty_calls_are_no_ops(lib):
     assert call(lib.paged_attention_decode_sparse, DECODE, S=0, q=None, out=None) == OK
 
 
-def test_one_block_call_refuses(lib):
-    args = list(DECODE.values())
-    for code, w, n in ((-1, words(args), 22), (4, words(args), 22), (3, None, 22),
-                       (3, words(args), 21), (2, words(args), 22)):
-        assert lib.kvp_call_words(code, w, n) == INVALID
-    for base, code, key in ((ROPE, 0, "T"), (ROPE, 0, "rot"), (BOUNDS, 1, "mcl"),
-                            (SELECT, 2, "keep"), (DECODE, 3, "cdt")):
-        args = list({**base, key: 2**32 + base[key]}.values())
-        assert lib.kvp_call_words(code, words(args), len(args)) == INVALID
-        assert b"out of range" in lib.kvp_last_error_message()
+def test_the_torch_binding_refuses_without_a_gpu():
+    import torch
+    import paged_kv_cache_319_b200 as kvp
+
+    x = torch.zeros((2, 2, 64), dtype=torch.float16)
+    pool = torch.zeros((4, 2, 16, 64), dtype=torch.float16)
+    t, l = torch.zeros((2, 1), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    idx = torch.zeros(2, dtype=torch.int64)
+    for call in (lambda: kvp.rope_reshape_and_cache(x, x, x, torch.zeros(8, 64), idx, pool, pool, idx),
+                 lambda: kvp.update_key_bounds(pool, pool[:, :, :2], t, l),
+                 lambda: kvp.select_blocks(x, pool[:, :, :2], t, l, block_size=16, num_selected=2),
+                 lambda: kvp.paged_attention_decode_sparse(x, pool, pool, t, l, t[:, None], 1.0)):
+        with pytest.raises(ValueError, match="same CUDA device"):
+            call()
+    with pytest.raises(TypeError, match="torch tensor"):
+        kvp.update_key_bounds([1], pool, t, l)
