@@ -18,8 +18,9 @@
 // legacy tensor-core path is nowhere near its limit (12% busy), and a tcgen05
 // tile would need 128 rows staged in shared memory first. What bounds a warp is
 // the latency of its chain of instructions per tile, so the softmax takes one
-// vote per tile and no reduction (32 sequences x 32 heads x 4096 tokens, bf16:
-// 125 us with a reduction and a rescaling per tile, 105 us without).
+// vote per tile and no reduction (32 sequences x 32 heads x 4096 tokens, bf16, on
+// 1,024 CTAs: 125 us with a reduction and a rescaling per tile, 105 without; 92 on
+// 256 CTAs).
 //
 // Operand layout. In m16n8k16, lane l holds rows l/4 and l/4 + 8 of A and, of
 // each row, the k positions 2p, 2p+1, 2p+8, 2p+9 (p = l % 4). A contraction may
@@ -459,7 +460,10 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT> * 32,
     }
   __syncthreads();
   const int heads = min(HEADS, G - h0);
-  for (int i = tid; i < heads * D; i += kThreads) {  // into warp 0's buffer
+  const float vs = FP8 ? __ldg(a.v_scale + g) : 1.f;
+  uint16_t* out = static_cast<uint16_t*>(a.out) +
+                  (int64_t(s) * a.num_q_heads + int64_t(g) * G + h0) * D;
+  for (int i = tid; i < heads * D; i += kThreads) {  // into warp 0's buffer, or out
     const int h = i / D;
     float mx = sm_m[h];
 #pragma unroll
@@ -468,17 +472,19 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT> * 32,
     float o = 0.f, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2f(sm_m[w * HEADS + h] - ms);
+      const float f = ex2(sm_m[w * HEADS + h] - ms);
       o += f * sm_acc[w * HEADS * D + i];
       sum += f * sm_l[w * HEADS + h];
+    }
+    if (nranks == 1) {
+      out[i] = Elem<T>::from_float(sum == 0.f ? 0.f : o * vs / sum);
+      continue;
     }
     sm_acc[i] = o;
     if (i % D == 0) part_m[h] = mx, part_l[h] = sum;
   }
+  if (nranks == 1) return;
   cluster.sync();
-  const float vs = FP8 ? __ldg(a.v_scale + g) : 1.f;
-  uint16_t* out = static_cast<uint16_t*>(a.out) +
-                  (int64_t(s) * a.num_q_heads + int64_t(g) * G + h0) * D;
   for (int i = rank * kThreads + tid; i < heads * D; i += nranks * kThreads) {
     const int h = i / D;
     float mx = -INFINITY;
@@ -486,7 +492,7 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT> * 32,
     const float ms = mx == -INFINITY ? 0.f : mx;
     float o = 0.f, sum = 0.f;
     for (uint32_t c = 0; c < nranks; ++c) {
-      const float f = exp2f(cluster.map_shared_rank(part_m, c)[h] - ms);
+      const float f = ex2(cluster.map_shared_rank(part_m, c)[h] - ms);
       o += f * cluster.map_shared_rank(sm_acc, c)[i];
       sum += f * cluster.map_shared_rank(part_l, c)[h];
     }

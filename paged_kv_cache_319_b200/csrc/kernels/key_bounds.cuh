@@ -8,13 +8,13 @@
 // Bound by HBM (a block's keys are read once, 2/block_size of that is
 // written). A warp takes heads_per_warp neighbouring heads of one block, whose
 // tiles are one contiguous run, so the chain of length, table entry and keys is
-// paid once per run; a tile is read with 16 bytes per lane and up to 8 loads in
-// flight. 32 contexts of 16,384 to 32,768 tokens x 8 heads (1.8 GB): 287 us;
-// with one head per warp 294, with 4 loads in flight as well 340.
+// paid once per run; a tile is read with 16 bytes per lane and 4 loads in flight,
+// so that enough warps fit an SM. 32 contexts of 16,384 to 32,768 tokens x 8 heads
+// (1.8 GB): 266 us, 6.8 TB/s; one head per warp 340, loads that bypass L1 284, 8 in
+// flight 267 (and 7.1 instead of 6.0 us for one block of 256 x 40 heads).
 #pragma once
 
 #include "common.cuh"
-#include "mma_sync.cuh"
 
 namespace kvp {
 namespace dev {
@@ -112,15 +112,15 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) key_bounds_kernel(const Bou
       hi[w] = MinMax2<T>::kInf2 | 0x80008000u;
       lo[w] = MinMax2<T>::kInf2;
     }
-    constexpr int U = 8;  // loads in flight per lane
+    constexpr int U = 4;  // loads in flight per lane
     for (int r0 = lane / LPR; r0 < rows; r0 += U * RPL) {
-      // a row past the context repeats the step's first one
       uint4 x[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        x[u] = ld_stream(tile + (r0 + u * RPL < rows ? r0 + u * RPL : r0) * LPR);
+        if (r0 + u * RPL < rows) x[u] = __ldg(tile + (r0 + u * RPL) * LPR);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        if (r0 + u * RPL >= rows) continue;
         const uint32_t p[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
         for (int w = 0; w < W; ++w) {

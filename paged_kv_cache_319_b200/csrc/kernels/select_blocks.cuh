@@ -13,12 +13,13 @@
 // Bound by HBM (the context's bounds are read once) if the scores cost little:
 // in fp64 a block's 2 D conversions and multiply-adds and the reduction over the
 // lanes took 4.4 times as long as its bytes (137 us for 32 x 8 rows of 1,500
-// blocks and D = 128; now 46, of them about 8 after the last byte). So the scores are first taken on the
-// tensor cores in fp32, 16 blocks (A rows) against the weights split into three
-// 16-bit parts (columns 0 to 2 of B), with a bound E on their error; only blocks
-// whose fp32 score lies within 2 E of the cut, usually a handful, are scored
-// in fp64. Where many lie there (equal blocks, a zero query) or E is not finite,
-// every block is.
+// blocks and D = 128; now 46, of them about 8 after the last byte). So the scores
+// are first taken on the tensor cores in fp32, 16 blocks (A rows) against the
+// weights split into three 16-bit parts (columns 0 to 2 of B), with a bound E on
+// their error; only blocks whose fp32 score lies within 2 E of the cut, usually a
+// handful, are scored in fp64. Where many lie there (equal blocks, a zero query) or
+// E is not finite, every block is; and so are all at once where there are only a
+// few (up to 64: 4 sequences x 4 heads of 38 blocks 7.2 -> 4.3 us).
 //
 // E: the weights are scaled by a power of two to at most 2^15, so three parts
 // leave 2^-24 of a weight or less; the MMAs' fp32 sums of 2 D products in steps
@@ -261,6 +262,61 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   const int32_t* table = a.block_tables + int64_t(s) * a.max_blocks_per_seq + a.sink + first;
   const bool gather = cand <= kSelMaxKeys;  // the first CTA selects alone
 
+  const int G = a.num_q_heads / a.num_kv_heads;
+  // the sum of a channel's weights over the group; comparisons that keep a NaN query
+  auto channel_weight = [&](int e) {
+    const bool low = e >= D;
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) +
+                        (int64_t(s) * a.num_q_heads + int64_t(g) * G) * D + (low ? e - D : e);
+    double w = 0.0;
+    for (int h = 0; h < G; ++h) {
+      const float f = Elem<TQ>::to_float2(__ldg(q + int64_t(h) * D)).x;
+      w += double(low ? (f > 0.f ? 0.f : f) : (f < 0.f ? 0.f : f));
+    }
+    return w;
+  };
+
+  // A few blocks: their fp64 scores at once, and every one's place by counting.
+  if (cand <= kSelNear) {
+    if (rank != 0) return;
+    for (int e = tid; e < 2 * D; e += kThreads) weight[e] = channel_weight(e);
+    __syncthreads();
+    constexpr int U = kSelNear / WARPS;
+    int at[U];
+    uint64_t k[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) at[u] = u * WARPS + warp < cand ? u * WARPS + warp : -1;
+    exact_keys<TB, D, U>(a, weight, table, at, g, k);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (lane == 0) sh.near_key[u * WARPS + warp] = k[u];
+    if (tid < cand) {
+      const int32_t b = __ldg(table + tid);
+      if ((b < 0 || b >= a.num_blocks) && g == 0)
+        record_error(KVP_DEVERR_BLOCK_ID, (uint64_t(s) << 32) | uint32_t(a.sink + tid));
+    }
+    __syncthreads();
+    bool kept = false;
+    if (tid < cand) {
+      const uint64_t mine = sh.near_key[tid];
+      uint32_t better = 0;
+      for (int i = 0; i < cand; ++i)
+        better += sh.near_key[i] > mine || (sh.near_key[i] == mine && i < tid);
+      kept = better < need;
+    }
+    if (tid < kSelNear) {
+      const uint32_t m = __ballot_sync(0xffffffffu, kept);
+      if (lane == 0) sh.take[0][warp] = m;
+    }
+    __syncthreads();
+    if (kept) {
+      uint32_t pos = a.sink + __popc(sh.take[0][warp] & ((1u << lane) - 1u));
+      for (int i = 0; i < warp; ++i) pos += __popc(sh.take[0][i]);
+      if (pos < uint32_t(a.keep)) out[pos] = a.sink + tid;
+    }
+    return;
+  }
+
   // the other CTAs' shared memory may be written once they have all started
   if (nranks > 1) ranks.cluster.barrier_arrive();
 
@@ -303,18 +359,9 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   int32_t id = locate(warp * 16), next = locate((warp + WARPS) * 16);
 
   // ---- weights: fp64 sums, and their three 16-bit parts ----
-  const int G = a.num_q_heads / a.num_kv_heads;
   float wmax = 0.f, wsum = 0.f;
   for (int e = tid; e < 2 * D; e += kThreads) {
-    const bool low = e >= D;
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) +
-                        (int64_t(s) * a.num_q_heads + int64_t(g) * G) * D + (low ? e - D : e);
-    double w = 0.0;
-    for (int h = 0; h < G; ++h) {
-      const float f = Elem<TQ>::to_float2(__ldg(q + int64_t(h) * D)).x;
-      // comparisons that keep a NaN query
-      w += double(low ? (f > 0.f ? 0.f : f) : (f < 0.f ? 0.f : f));
-    }
+    const double w = channel_weight(e);
     weight[e] = w;
     wmax = fmaxf(wmax, fabsf(float(w)));
   }

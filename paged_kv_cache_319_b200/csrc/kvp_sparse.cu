@@ -42,7 +42,7 @@ int launch_clusters(const char* fn, void (*kernel)(Args), int64_t units, int ran
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {unsigned(ranks), 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ranks > 1 ? 1 : 0;
   g_launched.store(true, std::memory_order_relaxed);
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
   return e == cudaSuccess ? KVP_OK : cuda_fail(e, fn);
