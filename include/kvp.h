@@ -695,8 +695,8 @@ KVP_API int select_blocks(const void* q, const void* key_bounds, const int32_t* 
  * [num_selected] holds logical block numbers in any order, negative entries
  * are skipped, a block listed twice counts twice; query heads of KV head h
  * attend to the tokens below context_lens[s] of the blocks in its list. A row
- * without such a token is zero. Keys and values of slots past the context are
- * not read. The pools are of dtype, or E4M3 (cache_dtype KVP_FP8_E4M3, with
+ * without such a token is zero. Slots past the context count for nothing,
+ * whatever they hold. The pools are of dtype, or E4M3 (cache_dtype KVP_FP8_E4M3, with
  * k_scale and v_scale [num_kv_heads] as in paged_attention_decode_fp8; NULL
  * otherwise). Any num_q_heads / num_kv_heads; softmax statistics and sums are
  * fp32.

@@ -10,8 +10,7 @@
 //
 // Bound by HBM: a listed block's keys and values are read once per KV head and
 // serve the whole group. Every warp works alone on tiles of 16 tokens (two
-// half tiles of 8, so blocks of 8, 16 and 32 tokens are alike): bulk copies
-// (cp.async.bulk; a block's rows of one head are contiguous) fill a ring of
+// half tiles of 8, so blocks of 8, 16 and 32 tokens are alike): TMA fills a ring of
 // stages of its own, and mma.sync multiplies from there. Keys and values are
 // the A operand (16 tokens, or 16 channels, by 16) and up to 8 query heads per
 // column tile the B operand: at the 2 to 32 FLOP per byte of this operator the
@@ -19,8 +18,10 @@
 // tile would need 128 rows staged in shared memory first. What bounds a warp is
 // the latency of its chain of instructions per tile, so the softmax takes one
 // vote per tile and no reduction (32 sequences x 32 heads x 4096 tokens, bf16, on
-// 1,024 CTAs: 125 us with a reduction and a rescaling per tile, 105 without; 92 on
-// 256 CTAs).
+// 1,024 CTAs: 125 us with a reduction and a rescaling per tile, 105 without), and
+// the tiles are swizzled, so that no read has a bank conflict (on 256 CTAs 92 us
+// with unswizzled bulk copies, 84 swizzled; 64 x 40 heads x 512 tokens, fp16: 97
+// and 87 us, 6.7 TB/s).
 //
 // Operand layout. In m16n8k16, lane l holds rows l/4 and l/4 + 8 of A and, of
 // each row, the k positions 2p, 2p+1, 2p+8, 2p+9 (p = l % 4). A contraction may
@@ -62,32 +63,31 @@ struct SparseArgs {
   float scale_log2;
 };
 
+// The pools as TMA maps: [rows][D] in boxes of min(block_size, 16) rows, 128-byte
+// swizzled, a 256-byte row as two segments ([segment][row][128 bytes]).
+struct SparseMaps {
+  CUtensorMap k, v;
+};
+
 constexpr int kChunk = 512;  // tiles located per pass over the list
 
-// Shared memory: 64 KiB of K/V stages, shared out among the warps (later the merge
-// area), then the located rows and valid tokens of kChunk tiles' halves, then the
-// barriers. A warp has two stages of 8 KiB (D = 128, 16-bit; three CTAs of four
-// warps per SM: a CTA's start and merge are covered by its neighbours' loads. 64
-// sequences x 40 heads x 512 tokens: 108 us; two CTAs with three stages 124, one
-// with six 182) or, of tiles half as large, two stages of 4 KiB in twice the warps.
-constexpr int kStageBytes = 64 * 1024;
-constexpr int kSmemBytes = kStageBytes + kChunk * 10 + 8 * 16 * 8;
+// Shared memory: the K/V stages, shared out among the warps (later the merge area),
+// then the located rows and valid tokens of kChunk tiles' halves, then the barriers.
+// A warp has two stages of 8 KiB (D = 128, 16-bit) or of 4 KiB. Many rows: 64 KiB of
+// stages, so that a CTA's start and merge are covered by its neighbours' loads (64
+// sequences x 40 heads x 512 tokens before the swizzle, two stages in three CTAs per
+// SM: 108 us; three stages in two CTAs 124, six in one 182). Few rows (WIDE): one CTA
+// per SM with twice the stages and warps, because a warp's chain per tile takes about
+// 1 us (3 sequences x 8 KV heads x 16,000 E4M3 tokens: 31 and 27 us).
+template <bool WIDE>
+constexpr int kStageBytes = (WIDE ? 128 : 64) * 1024;
+template <bool WIDE>
+constexpr int kSmemBytes = kStageBytes<WIDE> + kChunk * 10 + 16 * 16 * 8;
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-// Contiguous copy of `bytes` (a multiple of 16) into shared memory; completes
-// bar's transaction count. Addresses are 16-byte aligned.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1], %2, [%3], %4;" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
-      : "memory");
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -109,14 +109,14 @@ __device__ __forceinline__ uint32_t word(const uint4& x, int i) {
 }
 
 // Warps per CTA. The 16-head tiles' merge area leaves room for four.
-template <bool FP8, int D, int NT>
-constexpr int kSparseWarps = (FP8 || D == 64) && NT == 1 ? 8 : 4;
+template <bool FP8, int D, int NT, bool WIDE>
+constexpr int kSparseWarps = ((FP8 || D == 64) && NT == 1 ? 8 : 4) * (WIDE ? 2 : 1);
 
 // T: queries, output and products; FP8: E4M3 cache (D = 128); NT: tiles of 8 heads.
-template <typename T, bool FP8, int D, int NT>
-__global__ void __launch_bounds__(kSparseWarps<FP8, D, NT> * 32,
-                                  kSparseWarps<FP8, D, NT> == 4 && NT == 1 ? 3 : 2)
-    decode_sparse_kernel(const SparseArgs a) {
+template <typename T, bool FP8, int D, int NT, bool WIDE>
+__global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, WIDE> * 32,
+                                  WIDE ? 1 : kSparseWarps<FP8, D, NT, WIDE> == 4 && NT == 1 ? 3 : 2)
+    decode_sparse_kernel(const __grid_constant__ SparseMaps maps, const SparseArgs a) {
   namespace cg = cooperative_groups;
   constexpr int ROW = D * (FP8 ? 1 : 2);  // bytes of a cached row
   constexpr int KL = ROW / 64;            // 16-byte key loads per token row and lane
@@ -131,19 +131,19 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT> * 32,
   static_assert(!FP8 || D == 128, "E4M3 caches have head_dim 128");
 
   constexpr int TILE = 16 * ROW;                    // bytes of a tile's keys
-  constexpr int kWarps = kSparseWarps<FP8, D, NT>, kThreads = kWarps * 32;
-  constexpr int RING = kStageBytes / kWarps;  // bytes of a warp's stages
+  constexpr int kWarps = kSparseWarps<FP8, D, NT, WIDE>, kThreads = kWarps * 32;
+  constexpr int RING = kStageBytes<WIDE> / kWarps;  // bytes of a warp's stages
   constexpr int STAGES = RING / (2 * TILE);
-  static_assert(STAGES <= 16 && kStageBytes >= (kWarps * HEADS * (D + 2) + 2 * HEADS) * 4,
+  static_assert(STAGES <= 16 && kStageBytes<WIDE> >= (kWarps * HEADS * (D + 2) + 2 * HEADS) * 4,
                 "the merge area lies over the stages");
 
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ __align__(1024) unsigned char smem[];
   float* sm_acc = reinterpret_cast<float*>(smem);     // [kWarps][HEADS][D]
   float* sm_m = sm_acc + kWarps * HEADS * D;          // [kWarps][HEADS]
   float* sm_l = sm_m + kWarps * HEADS;
   float* part_m = sm_l + kWarps * HEADS;              // [HEADS], this CTA's merged partial
   float* part_l = part_m + HEADS;
-  uint2* rows = reinterpret_cast<uint2*>(smem + kStageBytes);  // [kChunk], a row per half
+  uint2* rows = reinterpret_cast<uint2*>(smem + kStageBytes<WIDE>);  // [kChunk], a row per half
   uint16_t* valid = reinterpret_cast<uint16_t*>(rows + kChunk);         // [kChunk], a byte per half
   uint64_t* bars = reinterpret_cast<uint64_t*>(valid + kChunk);         // [kWarps][16]
 
@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT> * 32,
                  (int64_t(s) * a.num_q_heads + int64_t(g) * G + (live ? h : 0)) * D;
 #pragma unroll
     for (int i = 0; i < QW / 4; ++i) {
-      // 16-bit rows: 8 channels at i*32 + p*8; E4M3 rows: 16 channels at (i/2)*64 + p*16
-      const int d = FP8 ? (i / 2) * 64 + p * 16 + (i & 1) * 8 : i * 32 + p * 8;
+      // the channels of the lane's 16-byte key reads, chunks 2p and 2p + 1 of a segment
+      const int d = FP8 ? (2 * p + (i >> 1)) * 16 + (i & 1) * 8 : (i >> 1) * 64 + (2 * p + (i & 1)) * 8;
       uint4 x = make_uint4(0, 0, 0, 0);
       if (live) x = __ldg(reinterpret_cast<const uint4*>(q + d));
       qf[t][4 * i] = x.x, qf[t][4 * i + 1] = x.y, qf[t][4 * i + 2] = x.z, qf[t][4 * i + 3] = x.w;
@@ -251,7 +251,11 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT> * 32,
   uint64_t* bar = bars + wid * 16;
   if (lane < STAGES) mbar_init(bar + lane, 1);
   fence_mbar_init();
-  const uint32_t stage0 = smem_u32(smem) + wid * RING;
+  unsigned char* ring = smem + wid * RING;
+  const uint32_t stage0 = smem_u32(ring);
+  // bytes between a tile's halves and between the segments of a row
+  const uint32_t half_bytes = bs >= 16 ? 1024 : TILE / 2, seg_bytes = bs >= 16 ? 2048 : 1024;
+  if (tid == 0) prefetch_tensormap(&maps.k), prefetch_tensormap(&maps.v);
   const uint64_t policy = l2_policy_evict_first();
   uint32_t phases = 0;  // parity of each stage's next completion
   bool alive = true;
@@ -269,22 +273,27 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT> * 32,
     }
     __syncthreads();
     const int mine = here / kWarps;
-    // loads of the warp's tile i into stage st; rows past the context are never read
+    // loads of the warp's tile i into stage st, whole boxes: slots past the context
+    // come along and are masked
     auto issue = [&](int i, int st) {
       const int j = i * kWarps + wid;
-      const uint32_t v = valid[j], va = v & 0xffu, vb = v >> 8;
+      const uint32_t v = valid[j];
       if (v == 0) return;
-      if (lane == 0) mbar_arrive_expect_tx(bar + st, (va + vb) * 2 * ROW);
+      const bool a0 = v & 0xffu, a1 = v >> 8;
+      if (lane == 0)
+        mbar_arrive_expect_tx(bar + st, bs >= 16 ? 2 * TILE : (uint32_t(a0) + uint32_t(a1)) * TILE);
       __syncwarp();
-      if (lane < 4) {  // lane bit 0: half tile, bit 1: keys or values
+      if (lane < (bs >= 16 ? 2 : 4)) {  // lane bit 0: keys or values, bit 1: half tile
         const uint2 row = rows[j];
-        const bool one = va == 8 && row.y == row.x + 8;  // neighbours: one copy
-        const uint32_t half = lane & 1;
-        const uint32_t n = half ? (one ? 0 : vb) : (one ? 8 + vb : va);
-        const char* src = static_cast<const char*>(lane >> 1 ? a.v_cache : a.k_cache);
-        if (n)
-          bulk_load(stage0 + st * 2 * TILE + (lane >> 1) * TILE + half * (TILE / 2),
-                    src + int64_t(half ? row.y : row.x) * ROW, n * ROW, bar + st, policy);
+        if (lane >> 1 ? a1 : (a0 || bs >= 16)) {
+          unsigned char* dst = ring + st * 2 * TILE + (lane & 1) * TILE + (lane >> 1) * (TILE / 2);
+          const CUtensorMap* map = lane & 1 ? &maps.v : &maps.k;
+          const int y = int(lane >> 1 ? row.y : row.x);
+          if constexpr (ROW == 256)
+            tma_load_3d(dst, map, bar + st, 0, y, 0, policy);
+          else
+            tma_load_2d(dst, map, bar + st, 0, y, policy);
+        }
       }
     };
     if (alive)
@@ -309,16 +318,22 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT> * 32,
       }
 
       uint4 kx[2][KL], vx[4][VL];
+      // 16-byte chunk c of a segment's row x is stored as chunk c ^ (x mod 8): the
+      // eight lanes of each quarter warp read eight different chunks
       const uint32_t ks = stage0 + st * 2 * TILE, vs = ks + TILE;
 #pragma unroll
       for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int j = 0; j < KL; ++j) kx[y][j] = lds128(ks + (y * 8 + r) * ROW + p * 16 + j * 64);
+        for (int j = 0; j < KL; ++j)
+          kx[y][j] = lds128(ks + y * half_bytes + (j >> 1) * seg_bytes + r * 128 +
+                            (((2 * p + (j & 1)) ^ r) << 4));
 #pragma unroll
-      for (int y = 0; y < 4; ++y)
+      for (int y = 0; y < 4; ++y) {
+        const uint32_t tok = 2 * p + (y & 1);
 #pragma unroll
         for (int j = 0; j < VL; ++j)
-          vx[y][j] = lds128(vs + ((y >> 1) * 8 + 2 * p + (y & 1)) * ROW + r * 16 + j * 128);
+          vx[y][j] = lds128(vs + (y >> 1) * half_bytes + j * seg_bytes + tok * 128 + ((r ^ tok) << 4));
+      }
       const bool partial = va + vb < 16;
       if (partial) {  // a stage's unfilled value rows hold anything
 #pragma unroll

@@ -27,6 +27,7 @@
 #include "pack_layout.h"
 #include "sparse.h"
 #include "status.h"
+#include "tensor_maps.h"
 #include "vcache.h"
 
 // Launch shape of the CUDA-core decode kernel: warps per CTA and TMA stages per
@@ -83,75 +84,6 @@
 #endif
 
 namespace {
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
-// 2-D view [rows][cols] of 2-byte elements with a {64, box_rows} box and
-// 128-byte swizzle; out-of-range rows read as zeros.
-int make_map(CUtensorMap* map, const void* base, int32_t dtype, uint64_t rows, uint64_t cols,
-             uint32_t box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return fail(KVP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * 2};
-  cuuint32_t box[2] = {64, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  const CUtensorMapDataType dt =
-      dtype == KVP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  CUresult r = fn(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(KVP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
-  return KVP_OK;
-}
-
-// 3-D view of [rows][128] 2-byte elements as {64 dims, rows, 2 halves} (strides
-// 256 and 128 bytes) with a {64, box_rows, 2} box: one load brings a whole
-// (block, head) tile as [half][row][64], 128-byte swizzled.
-int make_map_halves(CUtensorMap* map, const void* base, int32_t dtype, uint64_t rows,
-                    uint32_t box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return fail(KVP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  cuuint64_t dims[3] = {64, rows, 2};
-  cuuint64_t strides[2] = {256, 128};
-  cuuint32_t box[3] = {64, box_rows, 2};
-  cuuint32_t estr[3] = {1, 1, 1};
-  const CUtensorMapDataType dt =
-      dtype == KVP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  CUresult r = fn(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(KVP_ERR_CUDA, "cuTensorMapEncodeTiled (3-D) failed (%d)", int(r));
-  return KVP_OK;
-}
-
-// 2-D view [rows][128] of E4M3 codes with a {128, box_rows} box and 128-byte
-// swizzle: one load brings a whole (block, head) tile of head_dim 128.
-int make_map_u8(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return fail(KVP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  cuuint64_t dims[2] = {128, rows};
-  cuuint64_t strides[1] = {128};
-  cuuint32_t box[2] = {128, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
-                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(KVP_ERR_CUDA, "cuTensorMapEncodeTiled (E4M3) failed (%d)", int(r));
-  return KVP_OK;
-}
 
 // 4-D view of a virtually contiguous cache, {64 dims, tokens, 2 halves, KV
 // heads} with strides (Hkv * 256, 128, 256) bytes, and a {64, box_tokens,

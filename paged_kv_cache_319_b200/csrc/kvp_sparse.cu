@@ -4,9 +4,11 @@
 // caller's stream.
 #include <cuda_runtime.h>
 
+#include <array>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "kernels/common.cuh"
 #include "kernels/decode_sparse.cuh"
@@ -15,6 +17,7 @@
 #include "kernels/select_blocks.cuh"
 #include "launch_util.h"
 #include "sparse.h"
+#include "tensor_maps.h"
 
 namespace {
 
@@ -25,11 +28,12 @@ std::atomic<bool> g_launched{false};
 
 // Launch of `units` clusters of `ranks` CTAs along x; max_smem: the most dynamic
 // shared memory that any launch of this kernel takes.
-template <typename Args>
-int launch_clusters(const char* fn, void (*kernel)(Args), int64_t units, int ranks, int threads,
-                    int smem, int max_smem, const Args& args, cudaStream_t st) {
+template <typename... Args>
+int launch_clusters(const char* fn, void (*kernel)(Args...), int64_t units, int ranks, int threads,
+                    int smem, int max_smem, cudaStream_t st,
+                    const std::remove_const_t<Args>&... args) {
   if (units * ranks >= (int64_t(1) << 31)) return fail(KVP_ERR_INVALID, "%s: batch too large", fn);
-  if (smem > 32 * 1024) {  // beside up to 14 KiB of static shared memory
+  if (smem > 32 * 1024) {  // beside up to 16 KiB of static shared memory
     cudaError_t e = ensure_smem(kernel, max_smem);
     if (e != cudaSuccess) return cuda_fail(e, fn);
   }
@@ -44,8 +48,36 @@ int launch_clusters(const char* fn, void (*kernel)(Args), int64_t units, int ran
   cfg.attrs = attr;
   cfg.numAttrs = ranks > 1 ? 1 : 0;
   g_launched.store(true, std::memory_order_relaxed);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   return e == cudaSuccess ? KVP_OK : cuda_fail(e, fn);
+}
+
+// Clusters of `ranks` (1 to 8) CTAs that are on the current device at once, asked
+// once per kernel, device and size. The kernel's shared-memory limit has been raised.
+template <typename... Args>
+int resident_clusters(void (*kernel)(Args...), int ranks, int threads, int smem) {
+  static std::mutex mu;
+  static std::unordered_map<const void*, std::array<int, kMaxDevices * 8>> known;
+  const int d = current_device();
+  if (d < 0 || d >= kMaxDevices) return sm_count() / (2 * ranks);
+  std::lock_guard<std::mutex> guard(mu);
+  int& n = known[reinterpret_cast<const void*>(kernel)][d * 8 + ranks - 1];  // 0: not asked
+  if (n == 0) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(ranks));
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = size_t(smem);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {unsigned(ranks), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = 1;
+    }
+  }
+  return n;
 }
 
 // Checks that select_blocks and paged_attention_decode_sparse share.
@@ -123,14 +155,14 @@ int launch_select(const kvp::dev::SelectArgs& a, int head_dim, cudaStream_t st) 
   while (ranks < 8 && units * ranks < sm_count() && blocks >= 256 * ranks) ranks *= 2;
   if (head_dim == 64)
     return launch_clusters("select_blocks", kvp::dev::select_blocks_kernel<TQ, TB, 64, 8>, units,
-                           ranks, 256, smem, kSelMaxKeys * 8, a, st);
+                           ranks, 256, smem, kSelMaxKeys * 8, st, a);
   // one CTA per SM or fewer: twice the warps (8 rows of 8,192 blocks: 24.4 -> 20.9
   // us; 16 CTAs per row do not all fit the GPCs at once: 24.0); else two CTAs per SM, so that one may load while one selects
   return units * ranks <= sm_count() && blocks >= 256 * ranks
              ? launch_clusters("select_blocks", kvp::dev::select_blocks_kernel<TQ, TB, 128, 16>,
-                               units, ranks, 512, smem, kSelMaxKeys * 8, a, st)
+                               units, ranks, 512, smem, kSelMaxKeys * 8, st, a)
              : launch_clusters("select_blocks", kvp::dev::select_blocks_kernel<TQ, TB, 128, 8>,
-                               units, ranks, 256, smem, kSelMaxKeys * 8, a, st);
+                               units, ranks, 256, smem, kSelMaxKeys * 8, st, a);
 }
 
 template <typename T, bool FP8, int D, int NT>
@@ -140,13 +172,39 @@ int launch_sparse_nt(kvp::dev::sparse::SparseArgs a, cudaStream_t st) {
   a.head_tiles = (G + 8 * NT - 1) / (8 * NT);
   const int64_t units = int64_t(a.num_seqs) * a.num_kv_heads * a.head_tiles;
   const int64_t tiles = ((int64_t(a.num_selected) << a.log2_bs) + 15) / 16;
-  constexpr int warps = kSparseWarps<FP8, D, NT>;
+  SparseMaps maps;
+  const uint64_t rows = (uint64_t(a.num_blocks) * a.num_kv_heads) << a.log2_bs;
+  const uint32_t box = a.log2_bs == 3 ? 8 : 16;
+  const int32_t dtype = std::is_same<T, __half>::value ? KVP_F16 : KVP_BF16;
+  for (int i = 0; i < 2; ++i) {
+    CUtensorMap* map = i ? &maps.v : &maps.k;
+    const void* base = i ? a.v_cache : a.k_cache;
+    const int rc = FP8 ? make_map_u8(map, base, rows, box)
+                       : D == 128 ? make_map_halves(map, base, dtype, rows, box)
+                                  : make_map(map, base, dtype, rows, D, box);
+    if (rc) return rc;
+  }
+  constexpr int warps = kSparseWarps<FP8, D, NT, false>;
+  auto narrow = decode_sparse_kernel<T, FP8, D, NT, false>;
+  auto wide = decode_sparse_kernel<T, FP8, D, NT, true>;
+  constexpr int smem = kSmemBytes<false>, wide_smem = kSmemBytes<true>;
   // more CTAs per row while the rows alone leave SMs idle and each warp still has 2
   // tiles (256 rows of 4,096 tokens: one CTA each 93 us, two 99, four 105)
   int ranks = 1;
   while (ranks < 8 && units * ranks < sm_count() && tiles >= 4 * warps * ranks) ranks *= 2;
-  return launch_clusters("paged_attention_decode_sparse", decode_sparse_kernel<T, FP8, D, NT>,
-                         units, ranks, warps * 32, kSmemBytes, kSmemBytes, a, st);
+  if (units <= sm_count()) {
+    // few rows: CTAs of twice the warps, as many per row as are on the GPU at once
+    cudaError_t e = ensure_smem(wide, wide_smem);
+    if (e != cudaSuccess) return cuda_fail(e, "paged_attention_decode_sparse");
+    int r = 8;
+    while (r > 1 && (tiles < 4 * warps * r || units > resident_clusters(wide, r, warps * 64, wide_smem)))
+      --r;
+    if (2 * r > ranks && tiles >= 4 * warps * r)
+      return launch_clusters("paged_attention_decode_sparse", wide, units, r, warps * 64, wide_smem,
+                             wide_smem, st, maps, a);
+  }
+  return launch_clusters("paged_attention_decode_sparse", narrow, units, ranks, warps * 32, smem,
+                         smem, st, maps, a);
 }
 
 template <typename T, bool FP8, int D>
