@@ -171,6 +171,8 @@ int launch_sparse_nt(kvp::dev::sparse::SparseArgs a, cudaStream_t st) {
   const int G = a.num_q_heads / a.num_kv_heads;
   a.head_tiles = (G + 8 * NT - 1) / (8 * NT);
   const int64_t units = int64_t(a.num_seqs) * a.num_kv_heads * a.head_tiles;
+  if (units >= (int64_t(1) << 28))
+    return fail(KVP_ERR_INVALID, "paged_attention_decode_sparse: batch too large");
   const int64_t tiles = ((int64_t(a.num_selected) << a.log2_bs) + 15) / 16;
   SparseMaps maps;
   const uint64_t rows = (uint64_t(a.num_blocks) * a.num_kv_heads) << a.log2_bs;
