@@ -25,8 +25,8 @@
 // leave 2^-24 of a weight or less; the MMAs' fp32 sums of 2 D products in steps
 // of 16 are off by at most 2^-16 of the sum of the products' sizes even if each
 // addend is cut to 24 bits; S = max |bound| * sum |weight| is no less than that
-// sum, and E = 2^-15 S + 2^-117 (products below fp32's normal range) covers it
-// twice.
+// sum, and E = 2^-15 S covers it twice, with 2^-126 sum |weight| + 2^-117 for bounds
+// and products below fp32's normal range.
 //
 // One cluster of up to 8 CTAs serves a (sequence, KV head); each CTA scores a
 // contiguous range of blocks. The scores, as order-preserving keys, go straight to
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   lo32 = __reduce_min_sync(0xffffffffu, lo32);
   hi32 = __reduce_max_sync(0xffffffffu, hi32);
   big = __reduce_max_sync(0xffffffffu, big);
-  const float err = Elem<TB>::to_float2(big).x * wsum * 0x1p-15f + 0x1p-117f;
+  const float err = (Elem<TB>::to_float2(big).x * 0x1p-15f + 0x1p-126f) * wsum + 0x1p-117f;
   const bool finite = big < (std::is_same<TB, __half>::value ? 0x7c00u : 0x7f80u) &&
                       err < 0x1p126f && (wmax == 0.f || wmax >= 0x1p-126f);
 

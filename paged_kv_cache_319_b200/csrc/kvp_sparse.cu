@@ -377,7 +377,7 @@ int select_blocks(const void* q, const void* key_bounds, const int32_t* block_ta
                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                   int32_t num_blocks, int32_t max_blocks_per_seq, int32_t max_context_len,
                   int32_t num_selected, int32_t num_sink, int32_t num_recent, int32_t dtype,
-                  int32_t cache_dtype, kvp_stream_t stream) {
+                  int32_t cache_dtype, kvp_stream_t stream) try {
   const char* fn = "select_blocks";
   int rc = check_rows(fn, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
                       max_blocks_per_seq, max_context_len, num_selected, dtype, cache_dtype);
@@ -410,6 +410,8 @@ int select_blocks(const void* q, const void* key_bounds, const int32_t* block_ta
   if (dtype == KVP_F16) return launch_select<__half, __half>(a, head_dim, st);
   return cache_dtype == KVP_BF16 ? launch_select<__nv_bfloat16, __nv_bfloat16>(a, head_dim, st)
                                  : launch_select<__nv_bfloat16, __half>(a, head_dim, st);
+} catch (...) {  // the launch helpers' records take host memory
+  return fail(KVP_ERR_OOM, "select_blocks: no host memory");
 }
 
 int paged_attention_decode_sparse(const void* q, const void* k_cache, const void* v_cache,
@@ -420,7 +422,7 @@ int paged_attention_decode_sparse(const void* q, const void* k_cache, const void
                                   int32_t num_blocks, int32_t max_blocks_per_seq,
                                   int32_t max_context_len, int32_t num_selected, float scale,
                                   void* out, int32_t dtype, int32_t cache_dtype,
-                                  kvp_stream_t stream) {
+                                  kvp_stream_t stream) try {
   const char* fn = "paged_attention_decode_sparse";
   int rc = check_rows(fn, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
                       max_blocks_per_seq, max_context_len, num_selected, dtype, cache_dtype);
@@ -465,6 +467,8 @@ int paged_attention_decode_sparse(const void* q, const void* k_cache, const void
                             : launch_sparse<__nv_bfloat16, false, 128>(a, st);
   return dtype == KVP_F16 ? launch_sparse<__half, false, 64>(a, st)
                           : launch_sparse<__nv_bfloat16, false, 64>(a, st);
+} catch (...) {  // the launch helpers' records take host memory
+  return fail(KVP_ERR_OOM, "paged_attention_decode_sparse: no host memory");
 }
 
 }  // extern "C"

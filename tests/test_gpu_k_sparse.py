@@ -361,6 +361,25 @@ def test_selection_of_scores_closer_than_fp32_tells(n, close, dtype):
     assert np.array_equal(got.cpu().numpy()[0, 0], np.sort(np.argsort(-score, kind="stable")[:keep]))
 
 
+@pytest.mark.parametrize("dtype,quantum", [("f16", 2.0**-24), ("bf16", 2.0**-133), ("bf16", 2.0**110)])
+@pytest.mark.parametrize("n", [50, 900])
+def test_selection_of_tiny_and_huge_bounds(dtype, quantum, n):
+    # bounds of 1 to 127 quanta: below the type's normal range, or with sums past fp32's
+    kvp = _kvp()
+    rng = np.random.default_rng(45)
+    hi = rng.integers(1, 128, (n, 1, 64)) * quantum
+    bounds = np.stack([hi, -hi], 2)
+    qb = workloads.normal_bits([46, n], (1, 2, 64), dtype)
+    table = rng.permutation(n).astype(np.int32)[None]
+    bd = _dev(bounds).to(_tdt(dtype))
+    assert np.array_equal(to_f64(to_bits(bd), dtype), bounds)
+    got = kvp.select_blocks(from_bits(qb, dtype), bd, _dev(table), _dev(np.int32([n * 8])),
+                            block_size=8, num_selected=20)
+    kvp.check_device_error()
+    want = sparse.select_blocks(to_f64(qb, dtype), bounds, table, [n * 8], 8, 20, 1, 1)
+    assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_selection_reports_bad_metadata():
     torch, kvp = _torch(), _kvp()
     bounds = torch.rand((20, 1, 2, 64), device="cuda").half()
@@ -459,6 +478,47 @@ def test_decode_over_long_lists(Hq, Hkv, bs, dtype, cache, lens, keep):
                                             _dev(np.int32(lens)), _dev(sel), SCALE, **kw)
     kvp.check_device_error()
     _check_decode(to_bits(got), qb, vals, t, lens, sel, dtype, SCALE)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,bs,dtype,cache", [
+    (16, 1, 64, 16, "f16", "f16"), (4, 1, 64, 8, "bf16", "bf16"), (2, 1, 64, 32, "f16", "f16"),
+    (12, 1, 128, 16, "bf16", "e4m3"), (10, 1, 128, 8, "f16", "e4m3"), (5, 1, 128, 8, "bf16", "e4m3"),
+    (16, 1, 128, 32, "bf16", "bf16"), (11, 1, 128, 8, "f16", "f16"), (1, 1, 128, 16, "bf16", "bf16")])
+@pytest.mark.parametrize("seqs", [1, 21])
+def test_decode_of_few_rows_over_long_lists(Hq, Hkv, D, bs, dtype, cache, seqs):
+    kvp = _kvp()
+    lens = [6000 - 3 * s for s in range(seqs)]
+    qb, t, pools, vals, kw = _decode_case(63, lens, Hq, Hkv, D, bs, dtype, cache)
+    rng = np.random.default_rng(64)
+    keep = 4808 // bs
+    sel = np.stack([[np.sort(rng.permutation(-(-n // bs))[:keep]) for _ in range(Hkv)] for n in lens])
+    sel = sel.astype(np.int32)
+    got = kvp.paged_attention_decode_sparse(from_bits(qb, dtype), *pools, _dev(t),
+                                            _dev(np.int32(lens)), _dev(sel), 1 / np.sqrt(D), **kw)
+    kvp.check_device_error()
+    _check_decode(to_bits(got), qb, vals, t, lens, sel, dtype, 1 / np.sqrt(D))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_decode_of_large_and_tiny_queries_over_e4m3(dtype):
+    # bf16 queries far outside fp16's range, one head of zeros
+    torch, kvp = _torch(), _kvp()
+    lens = [200, 37]
+    qb, t, pools, vals, kw = _decode_case(65, lens, 4, 1, 128, 16, dtype, "e4m3")
+    factors = [1.0, 2.0**12, 2.0**-9, 0.0] if dtype == "f16" else [2.0**90, 2.0**-100, 1.0, 0.0]
+    q = from_bits(qb, dtype) * torch.tensor(factors, device="cuda", dtype=_tdt(dtype))[:, None]
+    sel = np.tile(np.arange(13, dtype=np.int32), (2, 1, 1))
+    sel[1, 0, 3:] = -1
+    # a scale per head cannot be given, so each factor's call uses its own
+    for h, f in enumerate(factors):
+        scale = SCALE / f if f else SCALE
+        got = kvp.paged_attention_decode_sparse(q[:, h:h + 1].contiguous(), *pools, _dev(t),
+                                                _dev(np.int32(lens)), _dev(sel), scale, **kw)
+        _check_decode(to_bits(got), to_bits(q[:, h:h + 1]), vals, t, lens, sel, dtype, scale)
+    both = kvp.paged_attention_decode_sparse(q, *pools, _dev(t), _dev(np.int32(lens)), _dev(sel),
+                                             SCALE, **kw)
+    kvp.check_device_error()
+    assert torch.isfinite(both[:, 2:]).all()
 
 
 @pytest.mark.parametrize("dtype,Hq,Hkv", [("f16", 4, 4), ("bf16", 8, 2)])
