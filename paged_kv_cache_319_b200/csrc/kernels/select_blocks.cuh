@@ -170,8 +170,7 @@ __device__ __forceinline__ int zoom(SelectShared& sh, SelectRanks& ranks, const 
   // the other buffer was last read before this call's ranks.sync
   for (int i = tid; i < kSelBins; i += WARPS * 32) sh.hist[phase ^ 1][i] = 0;
   __syncthreads();
-  uint32_t above = incl - total;
-  for (int i = 0; i < warp; ++i) above += sh.warp_sum[i];
+  uint32_t above = incl - total + __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sum[lane] : 0u);
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     if (above < need && above + bin[j] >= need)
@@ -641,11 +640,9 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
       }
       if (lane == 31) sh.warp_sum[warp] = incl;
       __syncthreads();
-      uint32_t pos = at + incl - __popc(mask);
-      for (int i = 0; i < WARPS; ++i) {
-        if (i < warp) pos += sh.warp_sum[i];
-        at += sh.warp_sum[i];
-      }
+      const uint32_t sums = lane < WARPS ? sh.warp_sum[lane] : 0u;
+      uint32_t pos = at + incl - __popc(mask) + __reduce_add_sync(0xffffffffu, lane < warp ? sums : 0u);
+      at += __reduce_add_sync(0xffffffffu, sums);
       for (; mask; mask &= mask - 1, ++pos)
         if (pos < uint32_t(a.keep)) out[pos] = a.sink + first + from + lane * 32 + __ffs(mask) - 1;
       __syncthreads();  // warp_sum is written again
