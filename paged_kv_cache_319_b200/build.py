@@ -9,7 +9,6 @@ tree; intermediate output (the ptxas report) goes to ``_build/``.
 from __future__ import annotations
 
 import argparse
-import concurrent.futures
 import importlib.util
 import os
 import shutil
@@ -31,7 +30,6 @@ SOURCES = [
     os.path.join(CSRC, "host", "group_plan.cpp"),
     os.path.join(CSRC, "host", "vcache.cpp"),
     os.path.join(CSRC, "kvp_device.cu"),
-    os.path.join(CSRC, "kvp_sparse.cu"),
 ]
 
 
@@ -63,35 +61,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
     tmp = LIB + ".tmp"
-    flags = [
-        "-std=c++17", "-O3", "-lineinfo", "-DNDEBUG",
+    cmds = [[
+        nvcc(), "-std=c++17", "-O3", "-lineinfo", "-DNDEBUG",
         "-gencode", "arch=compute_100a,code=sm_100a",
         "-Xcompiler", "-fPIC,-O3,-fvisibility=hidden",
         "-Xptxas", "-v",
         "-I", INCLUDE, "-I", CSRC,
-    ]
-    # one object per source, compiled side by side (kvp_device.cu takes minutes)
-    objects = [os.path.join(BUILD_DIR, os.path.basename(src) + ".o") for src in SOURCES]
-    jobs = [[nvcc()] + flags + ["-c", src, "-o", obj] for src, obj in zip(SOURCES, objects)]
-    with concurrent.futures.ThreadPoolExecutor(len(jobs)) as pool:
-        done = list(pool.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
-    cmds, out = jobs, "".join(r.stdout + r.stderr for r in done)
-    failed = any(r.returncode for r in done)
-    if not failed:
-        link = [nvcc()] + flags + ["-shared", "-o", tmp] + objects
-        res = subprocess.run(link, capture_output=True, text=True)
-        cmds, out, failed = cmds + [link], out + res.stdout + res.stderr, res.returncode != 0
+        "-shared", "-o", tmp,
+    ] + SOURCES]
+    res = subprocess.run(cmds[0], capture_output=True, text=True)
+    out, failed = res.stdout + res.stderr, res.returncode != 0
     if not failed:
         os.replace(tmp, LIB)
         # torch is needed for one header, DLPack's
         torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
-        link = [nvcc(), "-std=c++17", "-O3", "-gencode", "arch=compute_100a,code=sm_100a",
-                "-Xcompiler", "-fPIC,-O3,-fvisibility=hidden", "-I", INCLUDE,
-                "-I", os.path.join(torch_dir, "include"), "-I", sysconfig.get_paths()["include"],
-                "-shared", "-o", CALLS + ".tmp", CALLS_SOURCE, "-L", PKG, "-l:libkvp.so",
-                "-Xlinker", "-rpath", "-Xlinker", "$ORIGIN"]
-        res = subprocess.run(link, capture_output=True, text=True)
-        cmds, out, failed = cmds + [link], out + res.stdout + res.stderr, res.returncode != 0
+        cmds.append([
+            nvcc(), "-std=c++17", "-O3", "-gencode", "arch=compute_100a,code=sm_100a",
+            "-Xcompiler", "-fPIC,-O3,-fvisibility=hidden", "-I", INCLUDE,
+            "-I", os.path.join(torch_dir, "include"), "-I", sysconfig.get_paths()["include"],
+            "-shared", "-o", CALLS + ".tmp", CALLS_SOURCE, "-L", PKG, "-l:libkvp.so",
+            "-Xlinker", "-rpath", "-Xlinker", "$ORIGIN",
+        ])
+        res = subprocess.run(cmds[1], capture_output=True, text=True)
+        out, failed = out + res.stdout + res.stderr, res.returncode != 0
     with open(os.path.join(BUILD_DIR, "nvcc.log"), "w") as f:
         f.write("\n".join(" ".join(c) for c in cmds) + "\n\n" + out)
     if failed:

@@ -26,13 +26,10 @@ enum DevErr : uint32_t {
   KVP_DEVERR_CTX = 3,       // decode: context length outside [0, max_context_len]
   KVP_DEVERR_PAIR = 4,      // copy_blocks: src or dst outside [0, num_blocks)
   KVP_DEVERR_TIMEOUT = 5,   // a bounded wait ran out
-  KVP_DEVERR_POSITION = 6,  // rope_reshape_and_cache: position outside the table
-  KVP_DEVERR_SELECTED = 7,  // sparse decode: listed block past the context
 };
 
-// One word per translation unit of device code (kvp_device.cu, kvp_sparse.cu);
-// kvp_check_device_error reads and clears all of them.
-static __device__ unsigned long long g_error_word = 0ull;
+// Defined here: all device code is compiled as one translation unit.
+__device__ unsigned long long g_error_word = 0ull;
 
 __device__ __forceinline__ void record_error(uint32_t kind, uint64_t payload) {
   const unsigned long long v =

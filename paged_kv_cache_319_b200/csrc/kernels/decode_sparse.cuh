@@ -45,6 +45,9 @@ namespace kvp {
 namespace dev {
 namespace sparse {
 
+// Kind of the error word (beside DevErr's): listed block past the context.
+constexpr uint32_t KVP_DEVERR_SELECTED = 7;
+
 struct SparseArgs {
   const void* q;
   const void* k_cache;

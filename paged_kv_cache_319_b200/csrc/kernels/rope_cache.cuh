@@ -23,6 +23,9 @@
 namespace kvp {
 namespace dev {
 
+// Kind of the error word (beside DevErr's): position outside the table.
+constexpr uint32_t KVP_DEVERR_POSITION = 6;
+
 struct RopeArgs {
   const void* q;
   const void* k;

@@ -1,8 +1,8 @@
 // Device entry points of libkvp (C ABI): argument checks, TMA tensor maps,
 // kernel selection by geometry, launches on the caller's stream.
 //
-// The kernels are headers; those of block-sparse decoding are compiled by
-// kvp_sparse.cu, which has a device error word of its own.
+// All device code lives in this one translation unit (the kernels are
+// headers) so the device error word is a single symbol per GPU.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -23,12 +23,11 @@
 #include "kernels/decode_simt.cuh"
 #include "kernels/decode_tc.cuh"
 #include "kernels/prefill_tc.cuh"
-#include "launch_util.h"
 #include "pack_layout.h"
-#include "sparse.h"
 #include "status.h"
-#include "tensor_maps.h"
 #include "vcache.h"
+
+using kvp::fail;
 
 // Launch shape of the CUDA-core decode kernel: warps per CTA and TMA stages per
 // warp (shared memory per CTA = warps x stages x 2 tiles + merge area). The
@@ -84,6 +83,121 @@
 #endif
 
 namespace {
+
+constexpr int kMaxDevices = 64;
+
+int cuda_fail(cudaError_t e, const char* what) {
+  return fail(KVP_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+int current_device() {
+  int d = 0;
+  cudaGetDevice(&d);
+  return d;
+}
+
+int sm_count() {
+  static std::atomic<int> cache[kMaxDevices];
+  const int d = current_device();
+  if (d < 0 || d >= kMaxDevices) return 148;
+  int n = cache[d].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d);
+    if (n <= 0) n = 148;
+    cache[d].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Raises a kernel's dynamic shared-memory limit once per (kernel, device).
+template <typename K>
+cudaError_t ensure_smem(K kernel, int bytes) {
+  static std::mutex mu;
+  static std::unordered_map<const void*, uint64_t> done;  // kernel -> device bit mask
+  const int d = current_device();
+  const uint64_t bit = d < 64 ? (1ull << d) : 0;
+  const void* key = reinterpret_cast<const void*>(kernel);
+  {
+    std::lock_guard<std::mutex> g(mu);
+    auto it = done.find(key);
+    if (bit && it != done.end() && (it->second & bit)) return cudaSuccess;
+  }
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && bit) {
+    std::lock_guard<std::mutex> g(mu);
+    done[key] |= bit;
+  }
+  return e;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// 2-D view [rows][cols] of 2-byte elements with a {64, box_rows} box and
+// 128-byte swizzle; out-of-range rows read as zeros.
+int make_map(CUtensorMap* map, const void* base, int32_t dtype, uint64_t rows, uint64_t cols,
+             uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return fail(KVP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols * 2};
+  cuuint32_t box[2] = {64, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapDataType dt =
+      dtype == KVP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUresult r = fn(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(KVP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
+  return KVP_OK;
+}
+
+// 3-D view of [rows][128] 2-byte elements as {64 dims, rows, 2 halves} (strides
+// 256 and 128 bytes) with a {64, box_rows, 2} box: one load brings a whole
+// (block, head) tile as [half][row][64], 128-byte swizzled.
+int make_map_halves(CUtensorMap* map, const void* base, int32_t dtype, uint64_t rows,
+                    uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return fail(KVP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  cuuint64_t dims[3] = {64, rows, 2};
+  cuuint64_t strides[2] = {256, 128};
+  cuuint32_t box[3] = {64, box_rows, 2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt =
+      dtype == KVP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUresult r = fn(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(KVP_ERR_CUDA, "cuTensorMapEncodeTiled (3-D) failed (%d)", int(r));
+  return KVP_OK;
+}
+
+// 2-D view [rows][128] of E4M3 codes with a {128, box_rows} box and 128-byte
+// swizzle: one load brings a whole (block, head) tile of head_dim 128.
+int make_map_u8(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return fail(KVP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  cuuint64_t dims[2] = {128, rows};
+  cuuint64_t strides[1] = {128};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(KVP_ERR_CUDA, "cuTensorMapEncodeTiled (E4M3) failed (%d)", int(r));
+  return KVP_OK;
+}
 
 // 4-D view of a virtually contiguous cache, {64 dims, tokens, 2 halves, KV
 // heads} with strides (Hkv * 256, 128, 256) bytes, and a {64, box_tokens,
@@ -146,6 +260,14 @@ int make_map_prefill_q(CUtensorMap* map, const void* base, int32_t dtype, uint32
 #ifndef KVP_VCACHE_SIMT_TILE
 #define KVP_VCACHE_SIMT_TILE 16
 #endif
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int ilog2(int64_t v) {
+  int l = 0;
+  while ((int64_t(1) << l) < v) ++l;
+  return (int64_t(1) << l) == v ? l : -1;
+}
 
 struct Workspace {
   size_t ml_bytes, acc_bytes, total;
@@ -1433,17 +1555,10 @@ int kvp_check_device_error(kvp_stream_t stream) {
   unsigned long long v = 0;
   e = cudaMemcpyFromSymbol(&v, kvp::dev::g_error_word, sizeof(v));
   if (e != cudaSuccess) return cuda_fail(e, "kvp_check_device_error: read");
-  unsigned long long v2 = 0;  // the word of kvp_sparse.cu, cleared by this call
-  const int rc = kvp_sparse_take_error(&v2);
-  if (rc) return rc;
-  if (v == 0 && v2 == 0) return KVP_OK;
-  if (v) {
-    const unsigned long long zero = 0;
-    e = cudaMemcpyToSymbol(kvp::dev::g_error_word, &zero, sizeof(zero));
-    if (e != cudaSuccess) return cuda_fail(e, "kvp_check_device_error: clear");
-  } else {
-    v = v2;
-  }
+  if (v == 0) return KVP_OK;
+  const unsigned long long zero = 0;
+  e = cudaMemcpyToSymbol(kvp::dev::g_error_word, &zero, sizeof(zero));
+  if (e != cudaSuccess) return cuda_fail(e, "kvp_check_device_error: clear");
   const unsigned kind = unsigned(v >> 56);
   const unsigned long long payload = v & ((1ull << 56) - 1);
   static const char* names[] = {"none", "slot out of range (token index)",
@@ -1550,3 +1665,5 @@ extern "C" int paged_attention_decode_noalloc(
                                 max_blocks_per_seq, max_context_len, scale, partition_size, ws,
                                 need > 0 ? size_t(KVP_STATIC_SCRATCH_BYTES) : 0, out, dtype, stream);
 }
+
+#include "sparse_calls.h"

@@ -1,30 +1,19 @@
 // Entry points of block-sparse decoding (C ABI): the rotary append, the
 // per-block key bounds, the block selection and the decode over the selected
 // blocks. Argument checks, kernel selection by geometry, launches on the
-// caller's stream.
-#include <cuda_runtime.h>
+// caller's stream. Included at the end of kvp_device.cu, whose helpers and device
+// error word it shares.
+#pragma once
 
 #include <array>
-#include <atomic>
-#include <cmath>
-#include <cstdint>
 #include <type_traits>
 
-#include "kernels/common.cuh"
 #include "kernels/decode_sparse.cuh"
 #include "kernels/key_bounds.cuh"
 #include "kernels/rope_cache.cuh"
 #include "kernels/select_blocks.cuh"
-#include "launch_util.h"
-#include "sparse.h"
-#include "tensor_maps.h"
 
 namespace {
-
-// Whether this process has launched (or captured) a kernel of this file. Until then
-// its error word is clear, and reading it would load its module: right before a
-// timed loop of the other kernels that cost the loop 0.2 ms.
-std::atomic<bool> g_launched{false};
 
 // Launch of `units` clusters of `ranks` CTAs along x; max_smem: the most dynamic
 // shared memory that any launch of this kernel takes.
@@ -47,7 +36,6 @@ int launch_clusters(const char* fn, void (*kernel)(Args...), int64_t units, int 
   attr[0].val.clusterDim = {unsigned(ranks), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = ranks > 1 ? 1 : 0;
-  g_launched.store(true, std::memory_order_relaxed);
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   return e == cudaSuccess ? KVP_OK : cuda_fail(e, fn);
 }
@@ -123,7 +111,6 @@ template <typename T, bool FP8>
 int launch_rope(const kvp::dev::RopeArgs& a, dim3 grid, bool interleaved, cudaStream_t st) {
   auto k = interleaved ? kvp::dev::rope_cache_kernel<T, FP8, true>
                        : kvp::dev::rope_cache_kernel<T, FP8, false>;
-  g_launched.store(true, std::memory_order_relaxed);
   k<<<grid, kvp::dev::kRopeThreads, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? KVP_OK : cuda_fail(e, "rope_reshape_and_cache: launch");
@@ -132,7 +119,6 @@ int launch_rope(const kvp::dev::RopeArgs& a, dim3 grid, bool interleaved, cudaSt
 template <typename T, bool FP8, int D>
 int launch_bounds(const kvp::dev::BoundsArgs& a, int64_t warps, cudaStream_t st) {
   const int64_t ctas = (warps + kvp::dev::kBoundsWarps - 1) / kvp::dev::kBoundsWarps;
-  g_launched.store(true, std::memory_order_relaxed);
   kvp::dev::key_bounds_kernel<T, FP8, D><<<unsigned(ctas), kvp::dev::kBoundsWarps * 32, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? KVP_OK : cuda_fail(e, "update_key_bounds: launch");
@@ -217,17 +203,6 @@ int launch_sparse(const kvp::dev::sparse::SparseArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
-
-int kvp_sparse_take_error(unsigned long long* word) {
-  *word = 0;
-  if (!g_launched.load(std::memory_order_relaxed)) return KVP_OK;
-  cudaError_t e = cudaMemcpyFromSymbol(word, kvp::dev::g_error_word, sizeof(*word));
-  if (e != cudaSuccess) return cuda_fail(e, "kvp_check_device_error: read");
-  if (*word == 0) return KVP_OK;
-  const unsigned long long zero = 0;
-  e = cudaMemcpyToSymbol(kvp::dev::g_error_word, &zero, sizeof(zero));
-  return e == cudaSuccess ? KVP_OK : cuda_fail(e, "kvp_check_device_error: clear");
-}
 
 extern "C" {
 
