@@ -13,9 +13,11 @@
 // one token; a thread owns 16 channels (both ends of 8 pairs) of every row it
 // visits, so its 8 cosines and 8 sines are loaded once and stay in registers
 // while it walks the token's heads. 4 x 4,095 tokens of 32 + 8 heads into E4M3
-// (373 MB) take 67 us, 5.6 TB/s; what is left is the latency of slot, table row
-// and rows in turn. Four rows per thread in flight (80 registers) took 74 us, one
-// pass per CTA 77, CTAs that stay for many tokens 71.
+// (373 MB) take 64 us, 5.8 TB/s; what is left is the latency of slot, table row
+// and rows in turn, which many resident warps cover best: 12 CTAs per SM (40
+// registers) 64 us, 10 67, 16 66. Four rows per thread in flight (80 registers) took
+// 74 us, one pass per CTA 77, CTAs that stay for many tokens 71, and E4M3 codes by a
+// bracketed reciprocal instead of 16 divisions per item (56 registers) 69.
 #pragma once
 
 #include "common.cuh"
@@ -52,7 +54,7 @@ constexpr int kRopeThreads = 128;
 
 // T: 16-bit element; FP8: the cache holds E4M3 codes; PAIRED: interleaved pairs.
 template <typename T, bool FP8, bool PAIRED>
-__global__ void __launch_bounds__(kRopeThreads) rope_cache_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, FP8 ? 12 : 10) rope_cache_kernel(const RopeArgs a) {
   const int64_t t = blockIdx.x;
   const int64_t slot = __ldg(a.slots + t);
   const int64_t pos = __ldg(a.positions + t);
