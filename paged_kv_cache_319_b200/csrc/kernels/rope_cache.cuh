@@ -10,7 +10,7 @@
 // written in fp32 anywhere; one rounding to the stored type follows.
 //
 // Bound by HBM: each of q, k and v is read once and written once. A CTA serves
-// one token; a thread owns 16 channels (both ends of 8 pairs) of every row it
+// one token (or several, of few rows); a thread owns 16 channels (both ends of 8 pairs) of every row it
 // visits, so its 8 cosines and 8 sines are loaded once and stay in registers
 // while it walks the token's heads. 4 x 4,095 tokens of 32 + 8 heads into E4M3
 // (373 MB) take 64 us, 5.8 TB/s; what is left is the latency of slot, table row
@@ -48,28 +48,35 @@ struct RopeArgs {
   int32_t log2_ipr;  // items (16 channels) per row
   int32_t log2_bs;
   int32_t rows_per_cta;  // rows (heads of q, k, v) per CTA, grid.y slices
+  int32_t num_tokens;
+  int32_t log2_tpt;  // threads per token; fewer than a CTA's where a token has few rows
 };
 
-constexpr int kRopeThreads = 128;
+constexpr int kRopeLog2Threads = 7, kRopeThreads = 1 << kRopeLog2Threads;
 
-// T: 16-bit element; FP8: the cache holds E4M3 codes; PAIRED: interleaved pairs.
-template <typename T, bool FP8, bool PAIRED>
-__global__ void __launch_bounds__(kRopeThreads, FP8 ? 12 : 10) rope_cache_kernel(const RopeArgs a) {
-  const int64_t t = blockIdx.x;
+// T: 16-bit element; FP8: the cache holds E4M3 codes; PAIRED: interleaved pairs;
+// PACKED: several tokens per CTA (14,124 tokens of 3 rows of 64 channels: 15.7 -> 4.2
+// us; the general form costs the large case above 10 us in registers).
+template <typename T, bool FP8, bool PAIRED, bool PACKED>
+__global__ void __launch_bounds__(kRopeThreads, FP8 && !PACKED ? 12 : 10) rope_cache_kernel(const RopeArgs a) {
+  const int log2_tpt = PACKED ? a.log2_tpt : kRopeLog2Threads;
+  const int in_token = threadIdx.x & ((1 << log2_tpt) - 1);
+  const int64_t t = int64_t(blockIdx.x) * (kRopeThreads >> log2_tpt) + (threadIdx.x >> log2_tpt);
+  if (PACKED && t >= a.num_tokens) return;
   const int64_t slot = __ldg(a.slots + t);
   const int64_t pos = __ldg(a.positions + t);
   if (pos < 0 || pos >= a.max_positions) {
     // a padding token may carry any negative position; all else is a mistake
-    if (!(slot < 0 && pos < 0) && blockIdx.y == 0 && threadIdx.x == 0)
+    if (!(slot < 0 && pos < 0) && blockIdx.y == 0 && in_token == 0)
       record_error(KVP_DEVERR_POSITION, uint64_t(t));
     return;
   }
   const bool store_kv = slot >= 0 && slot < a.num_slots;
-  if (slot >= a.num_slots && blockIdx.y == 0 && threadIdx.x == 0)
+  if (slot >= a.num_slots && blockIdx.y == 0 && in_token == 0)
     record_error(KVP_DEVERR_SLOT, uint64_t(t));
 
-  const int j = threadIdx.x & ((1 << a.log2_ipr) - 1);
-  const int rows_per_pass = kRopeThreads >> a.log2_ipr;
+  const int j = in_token & ((1 << a.log2_ipr) - 1);
+  const int rows_per_pass = (1 << log2_tpt) >> a.log2_ipr;
   const int D = 16 << a.log2_ipr;
   const bool rotated = j * 16 < a.rot_dim;
   // the item's two runs of 8 channels
@@ -90,7 +97,7 @@ __global__ void __launch_bounds__(kRopeThreads, FP8 ? 12 : 10) rope_cache_kernel
 
   const int rows = a.num_q_heads + 2 * a.num_kv_heads;
   const int row_end = min(rows, int(blockIdx.y + 1) * a.rows_per_cta);
-  for (int row = blockIdx.y * a.rows_per_cta + (threadIdx.x >> a.log2_ipr); row < row_end;
+  for (int row = blockIdx.y * a.rows_per_cta + (in_token >> a.log2_ipr); row < row_end;
        row += rows_per_pass) {
     const bool is_q = row < a.num_q_heads;
     const bool is_v = row >= a.num_q_heads + a.num_kv_heads;

@@ -109,8 +109,11 @@ int log2_items(int32_t head_dim) { return head_dim % 16 ? -1 : ilog2(head_dim / 
 
 template <typename T, bool FP8>
 int launch_rope(const kvp::dev::RopeArgs& a, dim3 grid, bool interleaved, cudaStream_t st) {
-  auto k = interleaved ? kvp::dev::rope_cache_kernel<T, FP8, true>
-                       : kvp::dev::rope_cache_kernel<T, FP8, false>;
+  const bool packed = a.log2_tpt < kvp::dev::kRopeLog2Threads;
+  auto k = packed ? (interleaved ? kvp::dev::rope_cache_kernel<T, FP8, true, true>
+                                 : kvp::dev::rope_cache_kernel<T, FP8, false, true>)
+                  : (interleaved ? kvp::dev::rope_cache_kernel<T, FP8, true, false>
+                                 : kvp::dev::rope_cache_kernel<T, FP8, false, false>);
   k<<<grid, kvp::dev::kRopeThreads, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? KVP_OK : cuda_fail(e, "rope_reshape_and_cache: launch");
@@ -274,14 +277,20 @@ int rope_reshape_and_cache(const void* q, const void* k_new, const void* v_new, 
   a.rot_dim = rot_dim;
   a.log2_ipr = items;
   a.log2_bs = lbs;
-  // few tokens: a token's rows over several CTAs, one pass of each; many: one CTA per token
-  const int rows = num_q_heads + 2 * num_kv_heads, pass = kvp::dev::kRopeThreads >> items;
+  // threads per token: a CTA's, or as many as its few rows need
+  const int rows = num_q_heads + 2 * num_kv_heads;
+  a.num_tokens = num_tokens;
+  a.log2_tpt = items;
+  while (a.log2_tpt < kvp::dev::kRopeLog2Threads && (1 << (a.log2_tpt - items)) < rows) ++a.log2_tpt;
+  // few tokens: a token's rows over several CTAs, one pass of each; many: one pass after another
+  const int pass = (1 << a.log2_tpt) >> items, tokens = kvp::dev::kRopeThreads >> a.log2_tpt;
+  const int64_t ctas = (int64_t(num_tokens) + tokens - 1) / tokens;
   int64_t slices = (rows + pass - 1) / pass;
-  const int64_t wanted = (int64_t(8) * sm_count() + num_tokens - 1) / num_tokens;
+  const int64_t wanted = (int64_t(8) * sm_count() + ctas - 1) / ctas;
   if (slices > wanted) slices = wanted;
   if (slices > 65535) slices = 65535;
   a.rows_per_cta = int(((rows + slices - 1) / slices + pass - 1) / pass * pass);
-  const dim3 grid(unsigned(num_tokens), unsigned((rows + a.rows_per_cta - 1) / a.rows_per_cta));
+  const dim3 grid(unsigned(ctas), unsigned((rows + a.rows_per_cta - 1) / a.rows_per_cta));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (fp8)
     return dtype == KVP_F16 ? launch_rope<__half, true>(a, grid, interleaved != 0, st)
