@@ -62,7 +62,8 @@ struct SparseArgs {
   int32_t max_context_len;
   int32_t log2_bs;
   int32_t num_selected;
-  int32_t head_tiles;  // CTAs (clusters) per (sequence, KV head): ceil(G / (8 NT))
+  int32_t head_tiles;  // units per (sequence, KV head): ceil(G / (8 NT))
+  uint32_t num_units;  // served by a CTA, a cluster of them, or (SOLO) a warp each
   float scale_log2;
 };
 
@@ -115,12 +116,19 @@ __device__ __forceinline__ uint32_t word(const uint4& x, int i) {
 template <bool FP8, int D, int NT, bool WIDE>
 constexpr int kSparseWarps = ((FP8 || D == 64) && NT == 1 ? 8 : 4) * (WIDE ? 2 : 1);
 
+// How the rows are spread: a CTA or a cluster per unit; the same with wide CTAs; or a
+// warp per unit, for many rows of short lists: no merge, and a quarter of the CTAs.
+enum Spread { CTA, WIDE_CTA, SOLO };
+
 // T: queries, output and products; FP8: E4M3 cache (D = 128); NT: tiles of 8 heads.
-template <typename T, bool FP8, int D, int NT, bool WIDE>
-__global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, WIDE> * 32,
-                                  WIDE ? 1 : kSparseWarps<FP8, D, NT, WIDE> == 4 && NT == 1 ? 3 : 2)
+template <typename T, bool FP8, int D, int NT, Spread SPREAD>
+__global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, SPREAD == WIDE_CTA> * 32,
+                                  SPREAD == WIDE_CTA                        ? 1
+                                  : kSparseWarps<FP8, D, NT, false> == 4 && NT == 1 ? 3
+                                                                            : 2)
     decode_sparse_kernel(const __grid_constant__ SparseMaps maps, const SparseArgs a) {
   namespace cg = cooperative_groups;
+  constexpr bool WIDE = SPREAD == WIDE_CTA, ALONE = SPREAD == SOLO;
   constexpr int ROW = D * (FP8 ? 1 : 2);  // bytes of a cached row
   constexpr int KL = ROW / 64;            // 16-byte key loads per token row and lane
   constexpr int VL = ROW / 128;           // 16-byte value loads per token and lane
@@ -151,12 +159,13 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, WIDE> * 32,
   uint64_t* bars = reinterpret_cast<uint64_t*>(valid + kChunk);         // [kWarps][16]
 
   cg::cluster_group cluster = cg::this_cluster();
-  const uint32_t nranks = cluster.num_blocks(), rank = cluster.block_rank();
-  const uint32_t unit = blockIdx.x / nranks;
+  const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+  const uint32_t nranks = ALONE ? 1 : cluster.num_blocks(), rank = ALONE ? 0 : cluster.block_rank();
+  const uint32_t unit = ALONE ? blockIdx.x * kWarps + wid : blockIdx.x / nranks;
+  if (ALONE && unit >= a.num_units) return;  // a warp of its own: no barrier of the CTA follows
   const uint32_t ht = unit % a.head_tiles;
   const uint32_t sg = unit / a.head_tiles;
   const uint32_t s = sg / a.num_kv_heads, g = sg - s * a.num_kv_heads;
-  const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, p = lane & 3;
   const int G = a.num_q_heads / a.num_kv_heads;
   const int h0 = ht * HEADS;  // first head of the tile within the group
@@ -164,7 +173,7 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, WIDE> * 32,
 
   int ctx = __ldg(a.context_lens + s);
   if (ctx < 0 || ctx > a.max_context_len) {
-    if (g == 0 && ht == 0 && rank == 0 && tid == 0) record_error(KVP_DEVERR_CTX, s);
+    if (g == 0 && ht == 0 && rank == 0 && (ALONE ? lane : tid) == 0) record_error(KVP_DEVERR_CTX, s);
     ctx = ctx < 0 ? 0 : a.max_context_len;
   }
 
@@ -227,8 +236,11 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, WIDE> * 32,
   const int32_t* table = a.block_tables + int64_t(s) * a.max_blocks_per_seq;
   const int halves = a.num_selected << (a.log2_bs - 3);  // half tiles of 8 tokens
   const int tiles = (halves + 1) >> 1;
-  // tile j of this CTA is tile ((j / kWarps) * nranks + rank) * kWarps + j % kWarps of the list
-  const int rounds = (tiles + kWarps * int(nranks) - 1) / (kWarps * int(nranks));
+  // Tile j of this CTA is tile ((j / kWarps) * nranks + rank) * kWarps + j % kWarps of
+  // the list; a lone warp takes them all. `rounds`: tiles per warp.
+  const int rounds = ALONE ? tiles : (tiles + kWarps * int(nranks) - 1) / (kWarps * int(nranks));
+  constexpr int kPass = kChunk / kWarps;  // of them, located at a time
+  auto place = [&](int i) { return ALONE ? wid * kPass + i : i * kWarps + wid; };
 
   // cache row (block, head, slot) of half tile `half`, and its tokens below ctx
   auto locate = [&](int half, uint32_t& row, int& valid) {
@@ -258,28 +270,35 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, WIDE> * 32,
   const uint32_t stage0 = smem_u32(ring);
   // bytes between a tile's halves and between the segments of a row
   const uint32_t half_bytes = bs >= 16 ? 1024 : TILE / 2, seg_bytes = bs >= 16 ? 2048 : 1024;
-  if (tid == 0) prefetch_tensormap(&maps.k), prefetch_tensormap(&maps.v);
+  if ((ALONE ? lane : tid) == 0) prefetch_tensormap(&maps.k), prefetch_tensormap(&maps.v);
   const uint64_t policy = l2_policy_evict_first();
   uint32_t phases = 0;  // parity of each stage's next completion
   bool alive = true;
 
-  for (int j0 = 0; j0 < rounds * kWarps; j0 += kChunk) {
-    const int here = min(kChunk, rounds * kWarps - j0);
-    for (int j = tid; j < here; j += kThreads) {
-      const int t = (((j0 + j) / kWarps) * int(nranks) + int(rank)) * kWarps + j % kWarps;
+  auto sync = [&] {
+    if constexpr (ALONE)
+      __syncwarp();
+    else
+      __syncthreads();
+  };
+  for (int i0 = 0; i0 < rounds; i0 += kPass) {
+    const int mine = min(kPass, rounds - i0);
+    for (int j = ALONE ? lane : tid; j < (ALONE ? mine : mine * kWarps); j += ALONE ? 32 : kThreads) {
+      const int t = ALONE ? i0 + j
+                          : ((i0 + j / kWarps) * int(nranks) + int(rank)) * kWarps + j % kWarps;
       uint2 row;
       int va, vb;
       locate(2 * t, row.x, va);
       locate(2 * t + 1, row.y, vb);
-      rows[j] = row;
-      valid[j] = uint16_t(va | (vb << 8));
+      const int at = ALONE ? wid * kPass + j : j;
+      rows[at] = row;
+      valid[at] = uint16_t(va | (vb << 8));
     }
-    __syncthreads();
-    const int mine = here / kWarps;
+    sync();
     // loads of the warp's tile i into stage st, whole boxes: slots past the context
     // come along and are masked
     auto issue = [&](int i, int st) {
-      const int j = i * kWarps + wid;
+      const int j = place(i);
       const uint32_t v = valid[j];
       if (v == 0) return;
       const bool a0 = v & 0xffu, a1 = v >> 8;
@@ -307,14 +326,14 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, WIDE> * 32,
       fill = fill + 1 == STAGES ? 0 : fill + 1;
       __syncwarp();  // every lane has read the stage that is filled next
       if (i + STAGES - 1 < mine) issue(i + STAGES - 1, fill);
-      const int v = valid[i * kWarps + wid], va = v & 0xff, vb = v >> 8;
+      const int v = valid[place(i)], va = v & 0xff, vb = v >> 8;
       if (v == 0) continue;
       const bool ok = mbar_wait(bar + st, (phases >> st) & 1u, 0x5000u + st);
       phases ^= 1u << st;
       if (!__all_sync(0xffffffffu, ok)) {
         // give up: wait (each with the limit) for the copies in flight, read nothing
         for (int k = i + 1; k < min(mine, i + STAGES); ++k)
-          if (valid[k * kWarps + wid])
+          if (valid[place(k)])
             mbar_wait(bar + k % STAGES, (phases >> (k % STAGES)) & 1u, 0x5000u + st);
         alive = false;
         break;
@@ -455,7 +474,38 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, WIDE> * 32,
         }
       }
     }
-    __syncthreads();  // the located rows, or the stages, are written next
+    sync();  // the located rows, or the stages, are written next
+  }
+
+  const int heads = min(HEADS, G - h0);
+  const float vs = FP8 ? __ldg(a.v_scale + g) : 1.f;
+  uint16_t* out = static_cast<uint16_t*>(a.out) +
+                  (int64_t(s) * a.num_q_heads + int64_t(g) * G + h0) * D;
+
+  if constexpr (ALONE) {
+    // the lanes of a column have its sum; each writes its own channels
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float x = l[t][c];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        const int h = t * 8 + 2 * p + c;
+        if (h >= heads) continue;
+        const bool none = x == 0.f;
+        uint32_t w[MT];
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+          w[j] = Elem<T>::pack2(none ? 0.f : acc[t][j][c] * vs / x, none ? 0.f : acc[t][j][2 + c] * vs / x);
+#pragma unroll
+        for (int j = 0; j < MT; j += 4) {
+          const int d = FP8 ? r * 16 + 2 * j : (j / 4) * 64 + r * 8;
+          *reinterpret_cast<uint4*>(out + h * D + d) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+        }
+      }
+    return;
   }
 
   // ---- merge: lanes of a column, warps, CTAs ----
@@ -477,10 +527,6 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, WIDE> * 32,
       }
     }
   __syncthreads();
-  const int heads = min(HEADS, G - h0);
-  const float vs = FP8 ? __ldg(a.v_scale + g) : 1.f;
-  uint16_t* out = static_cast<uint16_t*>(a.out) +
-                  (int64_t(s) * a.num_q_heads + int64_t(g) * G + h0) * D;
   for (int i = tid; i < heads * D; i += kThreads) {  // into warp 0's buffer, or out
     const int h = i / D;
     float mx = sm_m[h];

@@ -176,9 +176,22 @@ int launch_sparse_nt(kvp::dev::sparse::SparseArgs a, cudaStream_t st) {
     if (rc) return rc;
   }
   constexpr int warps = kSparseWarps<FP8, D, NT, false>;
-  auto narrow = decode_sparse_kernel<T, FP8, D, NT, false>;
-  auto wide = decode_sparse_kernel<T, FP8, D, NT, true>;
+  auto narrow = decode_sparse_kernel<T, FP8, D, NT, CTA>;
+  auto wide = decode_sparse_kernel<T, FP8, D, NT, WIDE_CTA>;
+  auto solo = decode_sparse_kernel<T, FP8, D, NT, SOLO>;
   constexpr int smem = kSmemBytes<false>, wide_smem = kSmemBytes<true>;
+  a.num_units = uint32_t(units);
+  // A warp per row where lists are short (128 KiB of keys and values) and rows many:
+  // by the time of a start and a merge (about 4 us, of a lone warp 3) and of a tile
+  // (1 us per warp), in rounds of what is on the GPU at once. 154 x 40 rows of 5 tiles
+  // of 8 KiB 65 -> 38 us, 256 x 40 of up to 16 134 -> 104, 58 x 40 of up to 20 of 4 KiB
+  // 42 -> 24; 64 x 40 rows of up to 32 of 8 KiB lose, 87 -> 93.
+  const int64_t at_once = int64_t(sm_count()) * (NT == 1 && warps == 4 ? 3 : 2);
+  const int64_t cta_us = (units + at_once - 1) / at_once * (4 * warps + tiles) / warps;
+  const int64_t solo_us = (units + at_once * warps - 1) / (at_once * warps) * (3 + tiles);
+  if (tiles * 32 * D * (FP8 ? 1 : 2) <= 128 * 1024 && solo_us < cta_us)
+    return launch_clusters("paged_attention_decode_sparse", solo, (units + warps - 1) / warps, 1,
+                           warps * 32, smem, smem, st, maps, a);
   // more CTAs per row while the rows alone leave SMs idle and each warp still has 2
   // tiles (256 rows of 4,096 tokens: one CTA each 93 us, two 99, four 105)
   int ranks = 1;

@@ -480,6 +480,28 @@ def test_decode_over_long_lists(Hq, Hkv, bs, dtype, cache, lens, keep):
     _check_decode(to_bits(got), qb, vals, t, lens, sel, dtype, SCALE)
 
 
+@pytest.mark.parametrize("S,Hq,Hkv,D,bs,dtype,cache", [
+    (77, 41, 41, 128, 16, "f16", "f16"), (77, 41, 41, 64, 8, "bf16", "bf16"),
+    (97, 62, 31, 128, 8, "bf16", "bf16"), (97, 33, 33, 128, 32, "bf16", "e4m3"),
+    (600, 48, 4, 128, 16, "f16", "f16"), (601, 45, 5, 128, 8, "bf16", "e4m3"),
+    (600, 40, 4, 64, 32, "f16", "f16")])
+def test_decode_of_many_rows_over_short_lists(S, Hq, Hkv, D, bs, dtype, cache):
+    kvp = _kvp()
+    rng = np.random.default_rng(67)
+    lens = rng.integers(0, 5 * bs + 1, S).tolist()
+    qb, t, pools, vals, kw = _decode_case(68, lens, Hq, Hkv, D, bs, dtype, cache)
+    sel = np.full((S, Hkv, 5), -1, np.int32)
+    for s, n in enumerate(lens):
+        blocks = -(-n // bs)
+        for h in range(Hkv):
+            take = rng.permutation(blocks)[:rng.integers(0, blocks + 1)]
+            sel[s, h, rng.permutation(5)[:len(take)]] = take
+    got = kvp.paged_attention_decode_sparse(from_bits(qb, dtype), *pools, _dev(t),
+                                            _dev(np.int32(lens)), _dev(sel), SCALE, **kw)
+    kvp.check_device_error()
+    _check_decode(to_bits(got), qb, vals, t, lens, sel, dtype, SCALE)
+
+
 @pytest.mark.parametrize("Hq,Hkv,D,bs,dtype,cache", [
     (16, 1, 64, 16, "f16", "f16"), (4, 1, 64, 8, "bf16", "bf16"), (2, 1, 64, 32, "f16", "f16"),
     (12, 1, 128, 16, "bf16", "e4m3"), (10, 1, 128, 8, "f16", "e4m3"), (5, 1, 128, 8, "bf16", "e4m3"),
