@@ -120,12 +120,15 @@ constexpr int kSparseWarps = ((FP8 || D == 64) && NT == 1 ? 8 : 4) * (WIDE ? 2 :
 // warp per unit, for many rows of short lists: no merge, and a quarter of the CTAs.
 enum Spread { CTA, WIDE_CTA, SOLO };
 
+// CTAs per SM that the registers should allow.
+template <bool FP8, int D, int NT, Spread SPREAD>
+constexpr int kSparseCtas =
+    SPREAD == WIDE_CTA ? 1 : NT == 1 && kSparseWarps<FP8, D, NT, false> == 4 ? 3 : 2;
+
 // T: queries, output and products; FP8: E4M3 cache (D = 128); NT: tiles of 8 heads.
 template <typename T, bool FP8, int D, int NT, Spread SPREAD>
 __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, SPREAD == WIDE_CTA> * 32,
-                                  SPREAD == WIDE_CTA                        ? 1
-                                  : kSparseWarps<FP8, D, NT, false> == 4 && NT == 1 ? 3
-                                                                            : 2)
+                                  kSparseCtas<FP8, D, NT, SPREAD>)
     decode_sparse_kernel(const __grid_constant__ SparseMaps maps, const SparseArgs a) {
   namespace cg = cooperative_groups;
   constexpr bool WIDE = SPREAD == WIDE_CTA, ALONE = SPREAD == SOLO;
