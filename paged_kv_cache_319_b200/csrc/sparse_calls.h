@@ -295,6 +295,16 @@ int rope_reshape_and_cache(const void* q, const void* k_new, const void* v_new, 
   a.num_tokens = num_tokens;
   a.log2_tpt = items;
   while (a.log2_tpt < kvp::dev::kRopeLog2Threads && (1 << (a.log2_tpt - items)) < rows) ++a.log2_tpt;
+  // many tokens, 16-bit pools: fewer threads per token where that leaves fewer of them
+  // without a row in the last pass (25,000 tokens of 8 + 1 heads of 128: 35 -> 26 us; into
+  // E4M3 the packed kernel's registers cost more than it gains, 51 -> 55)
+  auto idle = [&](int log2_threads) {
+    const int per = 1 << (log2_threads - items);
+    return double((rows + per - 1) / per * per) / rows;
+  };
+  if (!fp8 && int64_t(num_tokens) >= int64_t(32) * sm_count())
+    for (int l = a.log2_tpt - 1; l >= items && l >= 5; --l)
+      if (idle(l) < idle(a.log2_tpt) - 0.1) a.log2_tpt = l;
   // few tokens: a token's rows over several CTAs, one pass of each; many: one pass after another
   const int pass = (1 << a.log2_tpt) >> items, tokens = kvp::dev::kRopeThreads >> a.log2_tpt;
   const int64_t ctas = (int64_t(num_tokens) + tokens - 1) / tokens;

@@ -83,6 +83,9 @@ def _append_case(seed, T, Hq, Hkv, D, rot, bs, NB, dtype, far=5000):
     (130, 6, 2, 128, 112, 16, "bf16", "e4m3", True),
     (2, 3, 1, 256, 256, 16, "bf16", "e4m3", False),
     (1500, 16, 4, 64, 48, 16, "bf16", "bf16", False),
+    (5003, 8, 1, 128, 64, 16, "bf16", "bf16", False),
+    (4999, 3, 1, 64, 16, 8, "f16", "f16", True),
+    (4801, 1, 1, 128, 128, 16, "f16", "e4m3", False),
 ])
 def test_append_rotates_and_stores(T, Hq, Hkv, D, rot, bs, dtype, cache, paired):
     torch, kvp = _torch(), _kvp()
