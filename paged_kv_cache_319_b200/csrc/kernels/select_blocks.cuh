@@ -26,7 +26,9 @@
 // of 16 are off by at most 2^-16 of the sum of the products' sizes even if each
 // addend is cut to 24 bits; S = max |bound| * sum |weight| is no less than that
 // sum, and E = 2^-15 S covers it twice, with 2^-126 sum |weight| + 2^-117 for bounds
-// and products below fp32's normal range.
+// and products below fp32's normal range. No partial sum exceeds S either, so E below
+// 2^111 (S below 2^126) keeps them all finite; bf16 bounds from 2^103 (many equal
+// weights) or 2^112 (one) on are scored in fp64.
 //
 // One cluster of up to 8 CTAs serves a (sequence, KV head); each CTA scores a
 // contiguous range of blocks. The scores, as order-preserving keys, go straight to
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   big = __reduce_max_sync(0xffffffffu, big);
   const float err = (Elem<TB>::to_float2(big).x * 0x1p-15f + 0x1p-126f) * wsum + 0x1p-117f;
   const bool finite = big < (std::is_same<TB, __half>::value ? 0x7c00u : 0x7f80u) &&
-                      err < 0x1p126f && (wmax == 0.f || wmax >= 0x1p-126f);
+                      err < 0x1p111f && (wmax == 0.f || wmax >= 0x1p-126f);
 
   // ---- the cut: keys above near_hi are kept, those below near_lo are not ----
   int phase = 0;
