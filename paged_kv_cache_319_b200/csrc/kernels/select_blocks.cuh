@@ -477,7 +477,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   big = __reduce_max_sync(0xffffffffu, big);
   const float err = (Elem<TB>::to_float2(big).x * 0x1p-15f + 0x1p-126f) * wsum + 0x1p-117f;
   const bool finite = big < (std::is_same<TB, __half>::value ? 0x7c00u : 0x7f80u) &&
-                      err < 0x1p111f && (wmax == 0.f || wmax >= 0x1p-126f);
+                      err < 0x1p111f && (wmax == 0.f || wmax >= 0x1p-126f) &&
+                      wmax < __int_as_float(0x7f800000);  // else a scaled part may be infinite
 
   // ---- the cut: keys above near_hi are kept, those below near_lo are not ----
   int phase = 0;

@@ -71,10 +71,67 @@ def test_selection_of_huge_bounds_of_one_sign(exponent, n, D, Hq, keep):
 @pytest.mark.parametrize("n,huge,keep", [(500, 12, (8, 40, 300)), (500, 200, (100, 250)),
                                          (3000, 70, (20, 200))])
 def test_selection_with_some_blocks_past_fp32(n, huge, keep):
-    # +2^115 and -2^115 in two channels cancel in fp64; in fp32 they are inf - inf
+    # +2^115 and -2^115 in two channels cancel in fp64; in fp32 they are inf - inf. What the
+    # other channels add is lost or not by the order of the fp64 sum, so these blocks may be
+    # kept or dropped: each of the 2 D additions is off by at most 2^-53 of the sum of the
+    # terms' sizes, and no kept block may lie further than both errors below a dropped one.
+    kvp = _kvp()
     rng = np.random.default_rng([n, huge])
     v = rng.standard_normal((n, 1, 64))
     at = rng.permutation(n)[:huge]
     v[at, 0, 0], v[at, 0, 4] = 2.0**115, -2.0**115
-    q = np.ones((1, 1, 64))
-    _check_selection(q, "bf16", np.stack([v, v], 2), "bf16", 8, keep)
+    qd, q = _put(np.ones((1, 1, 64)), "bf16")
+    bd, bounds = _put(np.stack([v, v], 2), "bf16")
+    table = np.random.default_rng(n).permutation(n).astype(np.int32)[None]
+    score = sparse.block_scores(q[0], bounds, table[0], n)[0]
+    err = 128 * 2.0**-53 * np.abs(bounds[table[0], 0, 0]).sum(1)
+    for k in keep:
+        got = kvp.select_blocks(qd, bd, _dev(table), _dev(np.int32([n * 8])), block_size=8,
+                                num_selected=k, num_sink=1, num_recent=1).cpu().numpy()[0, 0]
+        kvp.check_device_error()
+        assert got[0] == 0 and got[-1] == n - 1 and (np.diff(got) > 0).all()
+        kept = got[1:-1]
+        dropped = np.setdiff1d(np.arange(n), got)
+        assert (score + err)[kept].min() >= (score - err)[dropped].max()
+
+
+@pytest.mark.parametrize("n,huge,keep", [(500, 12, (8, 40, 300)), (500, 200, (100, 250)),
+                                         (3000, 70, (20, 200))])
+def test_selection_with_exact_sums_past_fp32(n, huge, keep):
+    # the same with the other channels multiples of 2^80: every fp64 sum is exact
+    rng = np.random.default_rng([n, huge])
+    v = rng.integers(-127, 128, (n, 1, 64)) * 2.0**80
+    at = rng.permutation(n)[:huge]
+    v[at, 0, 0], v[at, 0, 4] = 2.0**115, -2.0**115
+    _check_selection(np.ones((1, 1, 64)), "bf16", np.stack([v, v], 2), "bf16", 8, keep)
+
+
+@pytest.mark.parametrize("bounds_dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("Hq,keep", [(4, (90, 300)), (16, (30,))])
+def test_selection_of_query_groups_past_fp32(Hq, keep, bounds_dtype):
+    # the group's sum of a channel passes fp32's largest number though every query is finite
+    rng = np.random.default_rng([Hq, 71])
+    q = rng.uniform(1, 1.9, (1, Hq, 128)) * 2.0**127 * rng.choice([-1, 1], (1, 1, 128))
+    hi = rng.integers(-60, 127, (700, 1, 128)).astype(np.float64)
+    lo = hi - rng.integers(0, 60, hi.shape)
+    _check_selection(q, "bf16", np.stack([hi, lo], 2), bounds_dtype, 16, keep)
+
+
+@pytest.mark.parametrize("bounds_dtype", ["f16", "bf16"])
+def test_selection_of_query_groups_past_fp32_among_bad_block_ids(bounds_dtype):
+    # 60 of 100 table entries lie outside the pool and are scored last
+    kvp = _kvp()
+    rng = np.random.default_rng(76)
+    qd, q = _put(rng.uniform(1, 1.9, (1, 16, 128)) * 2.0**127, "bf16")
+    hi = rng.integers(1, 127, (100, 1, 128)).astype(np.float64)
+    bd, bounds = _put(np.stack([hi, hi], 2), bounds_dtype)
+    table = np.arange(100, dtype=np.int32)[None]
+    bad = rng.permutation(100)[:60]
+    table[0, bad] += 100
+    got = kvp.select_blocks(qd, bd, _dev(table), _dev(np.int32([1600])), block_size=16,
+                            num_selected=20, num_sink=0, num_recent=0).cpu().numpy()[0, 0]
+    with pytest.raises(kvp.KvpError):
+        kvp.check_device_error()
+    score = sparse.block_scores(q[0], bounds, np.arange(100), 100)[0]
+    score[bad] = -np.inf
+    assert np.array_equal(got, np.sort(np.argsort(-score, kind="stable")[:20]))
