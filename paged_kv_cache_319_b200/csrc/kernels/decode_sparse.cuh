@@ -402,7 +402,8 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, SPREAD == WIDE_CTA> *
       // ---- online softmax, per head (columns 2p, 2p + 1; rows r and r + 8) ----
       // The reference of the exponentials follows the maximum only when a logit
       // exceeds it by more than 8 (a factor 256, far inside fp16's range): one
-      // vote per tile instead of a reduction over the lanes and a rescaling.
+      // vote per tile instead of a reduction over the lanes and a rescaling. The
+      // difference is compared, since m + 8 rounds up where m has few bits below 8.
       bool rise = false;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, SPREAD == WIDE_CTA> *
         for (int e = 0; e < 4; ++e) {
           z[t][e] = (z[t][e] + z1[t][e]) * scale[t][e & 1];
           if (partial && r >= (e >> 1 ? vb : va)) z[t][e] = -INFINITY;
-          rise |= z[t][e] > m[t][e & 1] + 8.f;
+          rise |= z[t][e] - m[t][e & 1] > 8.f;
         }
       }
       if (__any_sync(0xffffffffu, rise)) {

@@ -135,3 +135,58 @@ def test_selection_of_query_groups_past_fp32_among_bad_block_ids(bounds_dtype):
     score = sparse.block_scores(q[0], bounds, np.arange(100), 100)[0]
     score[bad] = -np.inf
     assert np.array_equal(got, np.sort(np.argsort(-score, kind="stable")[:20]))
+
+
+# ---- paged_attention_decode_sparse --------------------------------------------------------
+# Rows that take the kernel's three forms: a cluster of wide CTAs, a CTA, and a warp per row.
+FORMS = [(1, 384), (200, 384), (3000, 6)]  # (sequences, 16-token tiles in the list)
+
+
+def _attend(q, q_dtype, k, v, cache, scale, seqs, **kw):
+    """Every sequence lists all blocks of the same context; keys and values [Hkv, tokens, D] in
+    blocks of 16. Returns row 0 and the values that the kernel read."""
+    torch, kvp = _torch(), _kvp()
+    Hkv, tokens, D = k.shape
+    NB = tokens // 16
+    kd, k = _put(np.ascontiguousarray(k.reshape(Hkv, NB, 16, D).transpose(1, 0, 2, 3)), cache)
+    vd, v = _put(np.ascontiguousarray(v.reshape(Hkv, NB, 16, D).transpose(1, 0, 2, 3)), cache)
+    qd, q = _put(q, q_dtype)
+    if cache == "e4m3":
+        for name in ("k_scale", "v_scale"):
+            kw[name] = _dev(np.float32(kw.get(name, np.ones(Hkv))))
+        k = k * kw["k_scale"].double().cpu().numpy()[:, None, None]
+        v = v * kw["v_scale"].double().cpu().numpy()[:, None, None]
+    table = torch.arange(NB, dtype=torch.int32, device="cuda").repeat(seqs, 1)
+    sel = table[:, None].repeat(1, Hkv, 1)
+    lens = torch.full((seqs,), tokens, dtype=torch.int32, device="cuda")
+    got = kvp.paged_attention_decode_sparse(qd[None].repeat(seqs, 1, 1), kd, vd, table, lens, sel,
+                                            float(scale), **kw)
+    kvp.check_device_error()
+    assert torch.equal(got, got[:1].expand_as(got))
+    return got[0].double().cpu().numpy(), (q[None], k, v, table[:1].cpu().numpy(), [tokens],
+                                           sel[:1].cpu().numpy(), float(scale))
+
+
+TYPES = [("f16", "f16"), ("bf16", "bf16"), ("f16", "e4m3"), ("bf16", "e4m3")]
+
+
+@pytest.mark.parametrize("seqs,tiles", FORMS)
+@pytest.mark.parametrize("dtype,cache", TYPES)
+def test_decode_of_logits_with_few_bits_below_one(dtype, cache, seqs, tiles):
+    # logits of 2^27, 2^27 + 16 and 2^27 + 32 in units of ln 2, neighbours in fp32: a reference
+    # that lags by 8 cannot be added to. The last third of the tokens has all the weight but
+    # 2^-16; what is left are the values' mean and its roundings.
+    rng = np.random.default_rng(72)
+    tokens = tiles * 16
+    third = np.arange(tokens) // (tokens // 3)
+    q, k = np.zeros((1, 128)), np.zeros((1, tokens, 128))
+    v = rng.integers(-8, 9, (1, tokens, 128)) / 8
+    kw = {}
+    if cache == "e4m3":
+        q[0, :2], k[0, :, 0], k[0, :, 1], kw["k_scale"] = [2.0**15, 1], 256, third, [16.0]
+    else:
+        q[0, :2], k[0, :, 0], k[0, :, 1] = [2.0**14, 16], 2.0**13, third
+    scale = np.float32(np.log(2.0))  # times log2(e) it is 1 in fp32
+    got, case = _attend(q, dtype, k, v, cache, scale, seqs, **kw)
+    ref = sparse.decode_sparse(*case)[0]
+    assert (np.abs(got - ref) <= half_ulp(ref, dtype) + 2.0**-15).all(), got
