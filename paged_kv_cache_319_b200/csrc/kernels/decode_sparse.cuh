@@ -141,7 +141,6 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, SPREAD == WIDE_CTA> *
   // type of the products: E4M3 values are fp16 values, so an E4M3 cache takes fp16
   // products (bf16 queries scaled by a power of two into its range)
   using M = typename std::conditional<FP8, __half, T>::type;
-  constexpr bool kSplitP = std::is_same<M, T>::value;  // weights in two parts
   constexpr bool kScaleQ = FP8 && !std::is_same<T, __half>::value;
   static_assert(!FP8 || D == 128, "E4M3 caches have head_dim 128");
 
@@ -441,17 +440,15 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, SPREAD == WIDE_CTA> *
           pr[e] = ex2(z[t][e] - (ref == -INFINITY ? 0.f : ref));
           l[t][e & 1] += pr[e];
         }
-        // p rounded once to the output's precision would cost as much again as the
-        // output's own rounding, so it goes as a high and a low part; fp16 products
-        // for a bf16 output have three bits to spare
+        // p rounded once to 16 bits would cost up to as much again as the output's own
+        // rounding (an eighth of it where fp16 products make a bf16 output), so it goes
+        // as a high and a low part
         const uint32_t hi0 = Elem<M>::pack2(pr[0], pr[1]), hi1 = Elem<M>::pack2(pr[2], pr[3]);
         pb[t][0] = transpose8x8(hi0);
         pb[t][1] = transpose8x8(hi1);
-        if constexpr (kSplitP) {
-          const float2 f0 = Elem<M>::to_float2(hi0), f1 = Elem<M>::to_float2(hi1);
-          pl[t][0] = transpose8x8(Elem<M>::pack2(pr[0] - f0.x, pr[1] - f0.y));
-          pl[t][1] = transpose8x8(Elem<M>::pack2(pr[2] - f1.x, pr[3] - f1.y));
-        }
+        const float2 f0 = Elem<M>::to_float2(hi0), f1 = Elem<M>::to_float2(hi1);
+        pl[t][0] = transpose8x8(Elem<M>::pack2(pr[0] - f0.x, pr[1] - f0.y));
+        pl[t][1] = transpose8x8(Elem<M>::pack2(pr[2] - f1.x, pr[3] - f1.y));
       }
 
       // ---- output: [channels][heads] += values^T * p ----
@@ -475,8 +472,7 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, SPREAD == WIDE_CTA> *
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           mma16816<M>(acc[t][j], af, pb[t][0], pb[t][1]);
-          if constexpr (kSplitP)
-            mma16816<M>(acc[t][j], af, pl[t][0], pl[t][1]);
+          mma16816<M>(acc[t][j], af, pl[t][0], pl[t][1]);
         }
       }
     }

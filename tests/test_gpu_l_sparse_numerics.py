@@ -190,3 +190,46 @@ def test_decode_of_logits_with_few_bits_below_one(dtype, cache, seqs, tiles):
     got, case = _attend(q, dtype, k, v, cache, scale, seqs, **kw)
     ref = sparse.decode_sparse(*case)[0]
     assert (np.abs(got - ref) <= half_ulp(ref, dtype) + 2.0**-15).all(), got
+
+
+def _weight_step(dtype, cache):
+    """Half a step of the weights in the second product: two 16-bit parts, of bf16 where the
+    cache is bf16, else of fp16; each is off by at most 2^-8 or 2^-11 of what it stands for."""
+    return 2.0**-16 if cache == "bf16" else 2.0**-22
+
+
+def _check_attend(got, case, dtype, cache, **kw):
+    ref = sparse.decode_sparse(*case)[0]
+    err = sparse.decode_error(*case, _weight_step(dtype, cache), **kw)[0]
+    bad = np.abs(got - ref) > err + half_ulp(np.abs(ref) + err, dtype)
+    assert not bad.any(), (bad.sum(), (np.abs(got - ref) / err).max())
+
+
+@pytest.mark.parametrize("seqs,tiles", FORMS)
+@pytest.mark.parametrize("dtype,cache", TYPES)
+def test_decode_of_weights_beside_a_half_step(dtype, cache, seqs, tiles):
+    # of 16 tokens one has weight 1 and the others 0.5 (1 + 0.98 h), h the half step of one
+    # 16-bit number: rounded to one, all of them lose 0.98 h
+    rng = np.random.default_rng(73)
+    tokens, Hkv = tiles * 16, 8
+    h = 2.0**-8 if cache == "bf16" else 2.0**-11
+    k = np.zeros((Hkv, tokens, 128))
+    k[:, np.arange(tokens) % 16 != 5, 0] = 1
+    q = np.zeros((2 * Hkv, 128))
+    q[:, 0] = 1
+    v = np.zeros((Hkv, tokens, 128)) + rng.uniform(1, 2, (Hkv, 1, 128))
+    v[:, np.arange(tokens) % 16 == 5] = 0
+    kw = {} if cache != "e4m3" else dict(v_scale=rng.uniform(1, 2, Hkv))
+    got, case = _attend(q, dtype, k, v, cache, np.log(0.5 * (1 + 0.98 * h)), seqs, **kw)
+    _check_attend(got, case, dtype, cache)
+
+
+@pytest.mark.parametrize("seqs,tiles", FORMS)
+@pytest.mark.parametrize("G", [1, 3, 12])
+@pytest.mark.parametrize("dtype,cache", TYPES)
+def test_decode_within_the_error_of_two_part_weights(dtype, cache, G, seqs, tiles):
+    rng = np.random.default_rng([74, G])
+    k, v = rng.standard_normal((2, 2, tiles * 16, 128))
+    kw = {} if cache != "e4m3" else dict(k_scale=[1.5, 0.7], v_scale=[0.8, 1.3])
+    got, case = _attend(rng.standard_normal((2 * G, 128)), dtype, k, v, cache, 128**-0.5, seqs, **kw)
+    _check_attend(got, case, dtype, cache)
