@@ -133,7 +133,7 @@ def listed(k_cache, v_cache, table, ctx: int, blocks, h: int):
 
 
 def decode_error(q, k_cache, v_cache, block_tables, context_lens, selected, scale: float,
-                 p_half_step: float) -> np.ndarray:
+                 p_half_step: float, p_floor: float = 2.0**-25) -> np.ndarray:
     """Bound on |fp32 kernel - exact| before the output's own rounding, ``[S, Hq, D]``.
 
     A logit is a sum of D fp32 products, off by at most dz = (D + 4) 2^-23 of the sum
@@ -142,7 +142,8 @@ def decode_error(q, k_cache, v_cache, block_tables, context_lens, selected, scal
     relative 2 dz or less (its own logit and the maximum's), plus ``p_half_step`` when
     it is rounded for the second product; the same 2 dz stands in the denominator. The
     second product and the merge add 2^-22 per accumulated term's share, below
-    2^-15 for 2^7 terms in a row. A weight below fp16's normal range is off by 2^-25."""
+    2^-15 for 2^7 terms in a row. A weight below fp16's normal range is off by
+    ``p_floor`` of the largest: 2^-25, or less where the largest is more than 1."""
     S, Hq, D = q.shape
     Hkv = k_cache.shape[1]
     G = Hq // Hkv
@@ -160,5 +161,5 @@ def decode_error(q, k_cache, v_cache, block_tables, context_lens, selected, scal
             p = np.exp(z - z.max(1, keepdims=True))
             size = p @ np.abs(V) / p.sum(1, keepdims=True)
             rel = 4 * dz[:, None] + p_half_step + 2.0**-15
-            out[s, h * G:(h + 1) * G] = size * rel + len(K) * 2.0**-25 * np.abs(V).max(0)
+            out[s, h * G:(h + 1) * G] = size * rel + len(K) * p_floor * np.abs(V).max(0)
     return out

@@ -141,6 +141,11 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, SPREAD == WIDE_CTA> *
   // type of the products: E4M3 values are fp16 values, so an E4M3 cache takes fp16
   // products (bf16 queries scaled by a power of two into its range)
   using M = typename std::conditional<FP8, __half, T>::type;
+  // The weights are 2^kLift at their reference and 2^(kLift + 8) at most, so fp16 parts
+  // reach down to 2^-(24 + kLift) of it; without the lift a long tail of weights below
+  // 2^-25 would vanish from the second product but not from the sum. bf16 has fp32's
+  // range. The factor is in the sums as well and cancels.
+  constexpr float kLift = std::is_same<M, __half>::value ? 7.f : 0.f;
   constexpr bool kScaleQ = FP8 && !std::is_same<T, __half>::value;
   static_assert(!FP8 || D == 128, "E4M3 caches have head_dim 128");
 
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, SPREAD == WIDE_CTA> *
   }
 
   float acc[NT][MT][4];
-  // m: the reference of the exponentials, a recent maximum; l: this lane's sum
+  // m: the reference of the exponentials, a recent maximum less kLift; l: this lane's sum
   float m[NT][2], l[NT][2];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, SPREAD == WIDE_CTA> *
 
       // ---- online softmax, per head (columns 2p, 2p + 1; rows r and r + 8) ----
       // The reference of the exponentials follows the maximum only when a logit
-      // exceeds it by more than 8 (a factor 256, far inside fp16's range): one
+      // exceeds it by more than 8 (a factor 256, so weights up to 2^15): one
       // vote per tile instead of a reduction over the lanes and a rescaling. The
       // difference is compared, since m + 8 rounds up where m has few bits below 8.
       bool rise = false;
@@ -410,7 +415,7 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, SPREAD == WIDE_CTA> *
         for (int e = 0; e < 4; ++e) {
           z[t][e] = (z[t][e] + z1[t][e]) * scale[t][e & 1];
           if (partial && r >= (e >> 1 ? vb : va)) z[t][e] = -INFINITY;
-          rise |= z[t][e] - m[t][e & 1] > 8.f;
+          rise |= z[t][e] - m[t][e & 1] > 8.f + kLift;
         }
       }
       if (__any_sync(0xffffffffu, rise)) {
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__(kSparseWarps<FP8, D, NT, SPREAD == WIDE_CTA> *
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float mn = fmaxf(m[t][c], mx);
+            const float mn = fmaxf(m[t][c], mx - kLift);
             const float alpha = mn == -INFINITY ? 1.f : ex2(m[t][c] - mn);
             m[t][c] = mn;
             l[t][c] *= alpha;

@@ -233,3 +233,23 @@ def test_decode_within_the_error_of_two_part_weights(dtype, cache, G, seqs, tile
     kw = {} if cache != "e4m3" else dict(k_scale=[1.5, 0.7], v_scale=[0.8, 1.3])
     got, case = _attend(rng.standard_normal((2 * G, 128)), dtype, k, v, cache, 128**-0.5, seqs, **kw)
     _check_attend(got, case, dtype, cache)
+
+
+@pytest.mark.parametrize("seqs,tiles", FORMS + [(1, 30)])
+@pytest.mark.parametrize("nats", [17.4, 18.5, 20.0])
+@pytest.mark.parametrize("dtype,cache", TYPES)
+def test_decode_of_one_strong_token_over_a_weak_tail(dtype, cache, nats, seqs, tiles):
+    # each of the others has a weight of 2^-25 to 2^-29 of the strong token's; in the even
+    # channels they are all there is
+    rng = np.random.default_rng(75)
+    tokens, strong = tiles * 16, tiles * 8 + 3
+    k = np.zeros((1, tokens, 128))
+    k[0, :, 0] = np.arange(tokens) != strong
+    q = np.zeros((1, 128))
+    q[0, 0] = 1
+    v = rng.integers(8, 16, (1, tokens, 128)) / 8
+    v[0, strong, ::2] = 0
+    got, case = _attend(q, dtype, k, v, cache, -nats, seqs)
+    # a part is off by at most 2^-25, half of fp16's smallest number, and the strongest
+    # weight is 2^7 or more; bf16 has fp32's range
+    _check_attend(got, case, dtype, cache, p_floor=0.0 if cache == "bf16" else 2.0**-32)
