@@ -4,6 +4,10 @@ torch tensors to it, in place with nvcc.
 Usage: ``python -m paged_kv_cache_319_b200.build [--force] [--verbose]``.
 They land next to this file so the package loads them from the source
 tree; intermediate output (the ptxas report) goes to ``_build/``.
+
+libkvp.so needs nvcc alone. The extension also needs Python's headers and a torch whose
+DLPack header has the C exchange table (2.11 has); without them it is left out, with a
+note, and only the calls that pass through it are missing.
 """
 
 from __future__ import annotations
@@ -42,10 +46,34 @@ def _inputs():
     return files
 
 
+def _calls_includes() -> list[str]:
+    """Include folders of the extension; raises FileNotFoundError, naming what is missing."""
+    python = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(python, "Python.h")):
+        raise FileNotFoundError("Python's headers are not installed")
+    spec = importlib.util.find_spec("torch")  # for one header, DLPack's
+    if spec is None or not spec.submodule_search_locations:
+        raise FileNotFoundError("torch is not installed")
+    torch = os.path.join(spec.submodule_search_locations[0], "include")
+    header = os.path.join(torch, "ATen", "dlpack.h")
+    if not os.path.exists(header):
+        raise FileNotFoundError("torch has no ATen/dlpack.h")
+    with open(header) as f:
+        if "DLPackExchangeAPI" not in f.read():
+            raise FileNotFoundError("torch's DLPack header has no exchange table")
+    return [torch, python]
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
+    built = [LIB]
+    try:
+        _calls_includes()
+        built.append(CALLS)
+    except FileNotFoundError:
+        pass
+    if not all(os.path.exists(f) for f in built):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
+    t = min(os.path.getmtime(f) for f in built)
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -71,14 +99,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
     ] + SOURCES]
     res = subprocess.run(cmds[0], capture_output=True, text=True)
     out, failed = res.stdout + res.stderr, res.returncode != 0
+    calls = False
     if not failed:
         os.replace(tmp, LIB)
-        # torch is needed for one header, DLPack's
-        torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+        try:
+            torch_include, python_include = _calls_includes()
+            calls = True
+        except FileNotFoundError as e:
+            sys.stderr.write(f"_torch_calls.so is not built, the block-sparse calls need it: {e}\n")
+            if os.path.exists(CALLS):  # made for another libkvp.so
+                os.remove(CALLS)
+    if calls:
         cmds.append([
             nvcc(), "-std=c++17", "-O3", "-gencode", "arch=compute_100a,code=sm_100a",
             "-Xcompiler", "-fPIC,-O3,-fvisibility=hidden", "-I", INCLUDE,
-            "-I", os.path.join(torch_dir, "include"), "-I", sysconfig.get_paths()["include"],
+            "-I", torch_include, "-I", python_include,
             "-shared", "-o", CALLS + ".tmp", CALLS_SOURCE, "-L", PKG, "-l:libkvp.so",
             "-Xlinker", "-rpath", "-Xlinker", "$ORIGIN",
         ])
@@ -89,7 +124,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if failed:
         sys.stderr.write(out)
         raise RuntimeError("nvcc failed; see " + os.path.join(BUILD_DIR, "nvcc.log"))
-    os.replace(CALLS + ".tmp", CALLS)
+    if calls:
+        os.replace(CALLS + ".tmp", CALLS)
     if verbose:
         sys.stdout.write(out)
     return LIB
