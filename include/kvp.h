@@ -627,7 +627,8 @@ KVP_API int paged_attention_decode_fp8(const void* q, const void* k_cache, const
  * rotated unless its position is negative too, in which case its row of q_out
  * stays as it was. Skipped whole and recorded (KVP_ERR_BOUNDS): a position
  * outside [0, max_positions) in any other token. Skipped keys and values and
- * recorded: a slot past the pool. Two tokens of one slot leave either's data.
+ * recorded: a slot past the pool. Two tokens of one slot leave a mixture of their
+ * keys and values, 8 channels or more from one token at a time.
  * head_dim / 16 (at most 64) and block_size are powers of two, rot_dim a
  * multiple of 16 in [16, head_dim].
  * Errors: KVP_ERR_INVALID (sizes, types, overlap, NULL or misaligned pointers). */

@@ -14,7 +14,7 @@
 // stages of its own, and mma.sync multiplies from there. Keys and values are
 // the A operand (16 tokens, or 16 channels, by 16) and up to 8 query heads per
 // column tile the B operand: at the 2 to 32 FLOP per byte of this operator the
-// legacy tensor-core path is nowhere near its limit (12% busy), and a tcgen05
+// legacy tensor-core path is nowhere near its limit (15 to 22% busy), and a tcgen05
 // tile would need 128 rows staged in shared memory first. What bounds a warp is
 // the latency of its chain of instructions per tile, so the softmax takes one
 // vote per tile and no reduction (32 sequences x 32 heads x 4096 tokens, bf16, on

@@ -18,7 +18,7 @@
 // weights split into three 16-bit parts (columns 0 to 2 of B), with a bound E on
 // their error; only blocks whose fp32 score lies within 2 E of the cut, usually a
 // handful, are scored in fp64. Where many lie there (equal blocks, a zero query) or
-// E is not finite, every block is; and so are all at once where there are only a
+// a fp32 sum could overflow, every block is; and so are all at once where there are only a
 // few (up to 64: 4 sequences x 4 heads of 38 blocks 7.2 -> 4.3 us).
 //
 // E: the weights are scaled by a power of two to at most 2^15, so three parts

@@ -296,8 +296,10 @@ int rope_reshape_and_cache(const void* q, const void* k_new, const void* v_new, 
   a.log2_tpt = items;
   while (a.log2_tpt < kvp::dev::kRopeLog2Threads && (1 << (a.log2_tpt - items)) < rows) ++a.log2_tpt;
   // many tokens, 16-bit pools: fewer threads per token where that leaves fewer of them
-  // without a row in the last pass (25,000 tokens of 8 + 1 heads of 128: 35 -> 26 us; into
-  // E4M3 the packed kernel's registers cost more than it gains, 51 -> 55)
+  // without a row in the last pass (25,000 tokens of 8 + 1 heads of 128: 35 -> 27 us). Into
+  // E4M3 the packed kernel has 10 CTAs per SM instead of 12, which costs more than it gains
+  // where many rows are codes (21,780 tokens of 8 + 8 heads 51 -> 55; of 8 + 1 it would
+  // gain, 38 -> 32)
   auto idle = [&](int log2_threads) {
     const int per = 1 << (log2_threads - items);
     return double((rows + per - 1) / per * per) / rows;
